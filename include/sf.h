@@ -741,6 +741,191 @@ sf_status sf_rope_kv_append_pair_cached(float* q, int Hq, uint16_t* q_bf16, floa
                                         uint16_t* v_scale, uint16_t* v_zero, sf_refine_cache* ref_cache,
                                         sf_stream_t stream, sf_stream_t side);
 
+/* ---- many requests: a paged 4-bit KV cache and per-request adapters ------ */
+
+/*
+ * A step of several requests at once.  The pages decode one request; these
+ * operators are the library's own addition for a program that serves many:
+ * each request's K and V live in fixed-size pages of one pool, a step adds a
+ * run of rows (tokens) per request, and per-request adapters go beside the
+ * shared low-bit projections.  One step, per layer after the plan:
+ *   sf_paged_plan      (once per step) lengths -> block table, slots, positions
+ *   sf_paged_append    RoPE of the rows' q and k, K and V quantized into pages
+ *   sf_attn_paged      attention of every row over its request's pages
+ *   sf_lora_add        a projection's output plus each row's low-rank adapter
+ * Rows are ordered by request: request i owns rows [cu_rows[i], cu_rows[i+1]).
+ * Sizes that only the device knows (lengths, row counts, page numbers, slots,
+ * adapter ids) are checked there; what falls outside is left out as stated per
+ * call and never read or written out of bounds.
+ */
+typedef enum sf_dtype { SF_F32 = 0, SF_BF16 = 1 } sf_dtype;
+
+/*
+ * The pool (device memory, caller-owned).  A page holds page_size consecutive
+ * tokens of one request, for every KV head:
+ *   *_codes uint32 [num_pages][Hkv][page_size][d/8]: 4-bit codes, code j of a
+ *           token-head at bits [4j, 4j+4) of its little-endian bitstream;
+ *   *_param uint32 [num_pages][Hkv][page_size]: the token-head's fp16 scale in
+ *           the low half and fp16 zero point in the high half; a key scale
+ *           whose bits are 0 marks a token that does not exist.
+ * Quantizer: sf_quantize_nested's with b = 4 and one group of d values per
+ * token-head; the value of code c is scale * (c - zero).
+ * page_rows: token-head rows from one page to the next in all four arrays
+ * (pages of several layers interleaved in one allocation); 0 means
+ * Hkv * page_size, otherwise at least that and a multiple of 4.
+ * Constraints: d in {64, 128, 256}, page_size a power of two in [16, 256],
+ * Hkv in [1, 256], num_pages >= 1, num_pages * page_size < 2^31; arrays
+ * 16-byte aligned.
+ */
+typedef struct sf_paged_kv {
+  uint32_t *k_codes, *k_param, *v_codes, *v_param;
+  int num_pages, Hkv, page_size, d;
+  int64_t page_rows;
+} sf_paged_kv;
+
+/*
+ * sf_paged_plan -- block table, slot map and free list of one step, from the
+ * requests' lengths, on the device.
+ *   Request i holds len[i] tokens, keeps the first keep[i] of them (all when
+ *   keep is NULL; 0 ends a request or hands its row to a new one; less than
+ *   len takes speculated tokens back) and adds add[i] rows.  With
+ *   have = ceil(len / page_size) and want = ceil((keep + add) / page_size):
+ *   pages want .. have-1 of its block-table row go back to the free list, or
+ *   pages have .. want-1 are taken from it and written to the row.
+ *   The free list is a stack, free_list[0 .. n_free): first every page given
+ *   back is pushed (requests in order, a request's pages in order), then the
+ *   a-th page taken (same order) is the a-th from the top.
+ * Outputs:
+ *   len_out[R]   keep + add (may be len itself);  n_free_out[1] (may be n_free);
+ *   block_table  [R][table_stride], the pages taken; other entries stay as they
+ *                are (those behind a request's last page are stale);
+ *   cu_rows[R+1] exclusive sums of add;
+ *   slots, positions, row_request [max_rows]: row r of request i is token
+ *                position = keep + r - cu_rows[i], slot = page * page_size +
+ *                position % page_size; rows behind the last: -1, 0, -1;
+ *   status[1]    SF_PLAN_OK, or why nothing was planned: SF_PLAN_LENGTH (len,
+ *                keep or add negative, keep > len, or a length above max_pages
+ *                * page_size), SF_PLAN_ROWS (more than max_rows rows),
+ *                SF_PLAN_PAGES (not enough free pages, or a free list that
+ *                would not fit free_cap).  Then len_out = len, n_free_out =
+ *                n_free, the table and list keep their values, cu_rows is all
+ *                0 and slots all -1, so that the step's other calls do nothing.
+ * Apart from the two pairs named, outputs must not overlap inputs.
+ * Constraints: 1 <= R <= 8192, page_size a power of two in [16, 256],
+ *   max_pages >= 1, max_pages * page_size < 2^31, table_stride >= max_pages,
+ *   max_rows >= 1, free_cap >= 1.
+ */
+enum { SF_PLAN_OK = 0, SF_PLAN_LENGTH = 1, SF_PLAN_ROWS = 2, SF_PLAN_PAGES = 3 };
+typedef struct sf_paged_plan_args {
+  const int32_t *len, *keep, *add; /* [R]; keep may be NULL */
+  int32_t* block_table;            /* [R][table_stride] */
+  int32_t* free_list;              /* [free_cap] */
+  const int32_t* n_free;           /* [1] */
+  int32_t *len_out, *n_free_out;   /* [R], [1] */
+  int32_t* cu_rows;                /* [R + 1] */
+  int32_t *slots, *positions, *row_request; /* [max_rows] */
+  int32_t* status;                 /* [1] */
+  int64_t table_stride;
+  int R, page_size, max_pages, max_rows, free_cap;
+} sf_paged_plan_args;
+sf_status sf_paged_plan(const sf_paged_plan_args* a, sf_stream_t stream);
+
+/*
+ * sf_paged_append -- quantizes the K and V rows of T tokens and writes them
+ * to their slots, optionally with RoPE of q and k in the same launch.
+ *   k, v     [T][Hkv][d] of src_type (SF_F32 or SF_BF16), rows k_stride and
+ *            v_stride elements apart (slices of a fused projection);
+ *   slots    int32 [T]; a row whose slot lies outside [0, num_pages *
+ *            page_size) is skipped whole.  Two rows with one slot leave
+ *            that slot's contents undefined.
+ *   theta    > 0: k (before it is quantized) and q are rotated to positions[t]
+ *            (int32 [T]) as sf_rope does, computed in fp64, k rounded once to
+ *            fp32, q once to bf16; k itself is not written.  q [T][Hq][d] of
+ *            src_type with rows q_stride apart goes to q_out (bf16, rows
+ *            q_out_stride apart); q NULL (Hq 0) rotates k alone.
+ *            0: no rotation; q, q_out NULL and Hq 0, positions not read.
+ *   k_val, v_val  NULL, or bf16 [T][Hkv][d]: receive the values that the pages
+ *            now hold for these rows (what attention over them will read).
+ * Values quantize as sf_kv_append does (finite sources).
+ * Constraints: kv's; 0 <= T; rows of k, v, q and q_out 16-byte aligned (base
+ *   and stride), strides at least a row, Hq <= 1024; theta >= 0 and finite.
+ */
+typedef struct sf_paged_append_args {
+  const sf_paged_kv* kv;
+  const void *k, *v, *q;
+  uint16_t *q_out, *k_val, *v_val;
+  const int32_t *slots, *positions;
+  int64_t k_stride, v_stride, q_stride, q_out_stride;
+  double theta;
+  int T, Hq, src_type;
+} sf_paged_append_args;
+sf_status sf_paged_append(const sf_paged_append_args* a, sf_stream_t stream);
+
+/*
+ * sf_attn_paged -- attention of a step's rows over a paged 4-bit cache.
+ *   Row j of request i (cu_rows[i] + j of q and out) is the token at position
+ *   p = len[i] - n_i + j, n_i the request's rows in this step; it attends to
+ *   tokens [0, p] of the request (the last `window` of them when window > 0)
+ *   that lie in pages: softmax(scale q . k) v, with K and V the values of the
+ *   4-bit codes.  Query head h reads KV head h / (Hq/Hkv).  A row with no token
+ *   to attend to gives zeros; rows from cu_rows[R] on are left as they were.
+ *   q       bf16 [T][Hq][d], rows q_stride elements apart;
+ *   out     [T][Hq][d] of out_type, rows out_stride elements apart;
+ *   len     int32 [R], tokens in the cache, this step's rows included; a length
+ *           outside [0, max_pages * page_size] counts as the nearer end;
+ *   block_table int32 [R][table_stride], max_pages entries per request; tokens
+ *           in pages outside [0, num_pages) are left out.
+ *   cu_rows int32 [R + 1], ascending; rows at or behind T are left out.
+ *   workspace device scratch of sf_attn_paged_workspace_size bytes, 16-byte
+ *           aligned, contents arbitrary, in use until the call's work ends.
+ * Scores are exact integer products of the codes with q in 22-bit fixed point
+ * relative to its row's largest entry; softmax weights enter the value product
+ * as f16 pairs (22 bits); all sums are fp32.  The order of sums is fixed by
+ * the arguments' values, so equal calls give equal bits.
+ * Constraints: kv's; Hq a multiple of Hkv, Hq/Hkv <= 64, 1 <= R <= 8192,
+ *   T >= 0, max_pages >= 1, max_pages * page_size < 2^31, window >= 0, scale
+ *   finite; rows of q and out 16-byte aligned.
+ */
+typedef struct sf_attn_paged_args {
+  const sf_paged_kv* kv;
+  const uint16_t* q;
+  const int32_t *cu_rows, *len, *block_table;
+  void *out, *workspace;
+  size_t ws_bytes;
+  int64_t q_stride, out_stride, table_stride;
+  float scale;
+  int T, R, Hq, max_pages, window, out_type;
+} sf_attn_paged_args;
+sf_status sf_attn_paged_workspace_size(int T, int R, int Hq, int Hkv, int d, size_t* bytes);
+sf_status sf_attn_paged(const sf_attn_paged_args* a, sf_stream_t stream);
+
+/*
+ * sf_lora_add -- low-rank adapters of many requests beside one projection:
+ *   out[t] = y[t] + scale[a] * B_a (A_a x[t]),  a = ids[row_of[t]],
+ * for every row t < T (row_of NULL: a = ids[t]; with sf_paged_plan's
+ * row_request, ids is per request).  A row whose row_of lies outside [0,
+ * n_ids) or whose id lies outside [0, n_adapters) has no adapter: out[t] = y[t].
+ *   x   bf16 [T][K];  y, out fp32 [T][N] (out may be y; y NULL means 0);
+ *   A   bf16 [n_adapters][rank][K];  B bf16 [n_adapters][N][rank];
+ *   scale fp32 [n_adapters].  Rows of x, y and out are *_stride elements apart.
+ * An adapter of a smaller rank is padded with zero rows of A.
+ * A x is kept in fp32 (it enters the second product as three bf16 terms, 24
+ * bits); all sums are fp32 in a fixed order.
+ * Constraints: T >= 0, n_ids >= 0, n_adapters >= 1, N >= 1, K a positive
+ *   multiple of 8, rank a multiple of 8 in [8, 128]; A, B 16-byte aligned, rows
+ *   of x 16-byte aligned, strides at least a row.
+ */
+typedef struct sf_lora_args {
+  const uint16_t *x, *A, *B;
+  const float* scale;
+  const int32_t *ids, *row_of;
+  const float* y;
+  float* out;
+  int64_t x_stride, y_stride, out_stride;
+  int T, n_ids, n_adapters, K, N, rank;
+} sf_lora_args;
+sf_status sf_lora_add(const sf_lora_args* a, sf_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -6,7 +6,8 @@ of ``libsf.so``.  PyTorch provides device memory and the current CUDA stream.
 The functions mirror the C ABI declared in ``include/sf.h``:
 
   quantize_nested, select_topk, gemv_refine, attn_decode_refine,
-  attn_workspace_size, RefineCache (sf_refine_cache_*).
+  attn_workspace_size, RefineCache (sf_refine_cache_*); for a step of many
+  requests PagedPlan, PagedAppend, PagedAttention and LoraAdd (``serving``).
 
 Importing fails loudly when the library has not been built (``build()`` in
 ``quantized_gemv_kv_b200.build``); there is no CPU fallback.
@@ -127,6 +128,11 @@ _SIGS = {
     "sf_kv_append_pair_cached": ([_p, _p, _i, _i, _i, _i, _i, _i, _p, _p, _p, _p, _p, _p, _p, _p, _p], _i),
     "sf_rope_kv_append_pair_cached": ([_p, _i, _p, _p, _p, _i, _i, _i, ctypes.c_double, _i, _i, _i, _i, _p, _p, _p,
                                        _p, _p, _p, _p, _p, _p], _i),
+    "sf_paged_plan": ([_p, _p], _i),
+    "sf_paged_append": ([_p, _p], _i),
+    "sf_attn_paged_workspace_size": ([_i, _i, _i, _i, _i, ctypes.POINTER(_sz)], _i),
+    "sf_attn_paged": ([_p, _p], _i),
+    "sf_lora_add": ([_p, _p], _i),
 }
 for _name, (_args, _res) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -784,3 +790,10 @@ def gemv_fp16_fetch(W: QWeight, x: torch.Tensor, idx: torch.Tensor, n: torch.Ten
     _check(_lib.sf_gemv_fp16_fetch(ctypes.byref(s), _ptr(x), B, _ptr(idx), _ptr(n), _ptr(resid),
                                    cache.handle if cache is not None else None, _ptr(y), _stream(stream)))
     return y
+
+
+# ---- many requests: the paged 4-bit cache and per-request adapters -----------------
+
+from .serving import (  # noqa: E402
+    PLAN_LENGTH, PLAN_OK, PLAN_PAGES, PLAN_ROWS, LoraAdd, PagedAppend, PagedAttention, PagedKV, PagedPlan,
+    attn_paged, attn_paged_workspace_size, lora_add, paged_append, paged_plan)

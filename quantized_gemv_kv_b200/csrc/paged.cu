@@ -1,0 +1,463 @@
+// The step's bookkeeping for a paged 4-bit KV cache (sf_paged_plan) and the
+// append of its rows (sf_paged_append).
+#include <algorithm>
+#include <cmath>
+
+#include <cooperative_groups.h>
+
+#include "paged.cuh"
+#include "produce.cuh"
+
+namespace {
+
+namespace cg = cooperative_groups;
+
+// ---- sf_paged_plan ------------------------------------------------------------
+//
+// Three exclusive sums over the requests (rows added, pages taken, pages
+// given back) decide everything: row r, the a-th page taken and the f-th page
+// given back each find their request by a binary search in one of them.  The
+// work is a few integers per row, so the kernel is bound by latency: one
+// thread-block cluster does it all in one launch.  Every CTA of the cluster
+// takes the sums over all requests itself (R <= 8192: three loads per request
+// from L2, cheaper than an exchange), keeps them in shared memory, and does
+// its share of the rows and pages.  The one cluster barrier separates every
+// read of the lengths and the pushes onto the free list from the writes that
+// may alias or follow them, so the lengths and the free count can be updated
+// in place; what the rows need of a request after it is kept in shared memory.
+
+constexpr int kPlanMaxR = 8192;
+
+struct PlanArgs {
+  sf_paged_plan_args a;
+  int shift;  // log2(page_size)
+};
+
+// Index of the last entry of ascending cum[0..R] that is <= v (cum[0] = 0,
+// v < cum[R]): the request that owns element v.
+__device__ __forceinline__ int owner_of(const int* cum, int R, int v) {
+  int lo = 0, hi = R;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (cum[mid] <= v)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+// Shared-memory integers per request: three sums, the tokens kept, the pages held.
+constexpr int kPlanArrays = 5;
+
+__global__ void __launch_bounds__(1024) paged_plan_kernel(const __grid_constant__ PlanArgs P) {
+  extern __shared__ int sh[];
+  const sf_paged_plan_args& a = P.a;
+  const int R = a.R, shift = P.shift, tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
+  int* cu = sh;           // [R + 1] rows before request i
+  int* ct = cu + R + 1;   // [R + 1] pages taken before it
+  int* cb = ct + R + 1;   // [R + 1] pages given back before it
+  int* kp = cb + R + 1;   // [R] tokens kept
+  int* hv = kp + R;       // [R] pages held
+  __shared__ long long part[32][3];
+  __shared__ int bad_sh;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int nthreads = nt * static_cast<int>(cluster.num_blocks());
+  const int gtid = static_cast<int>(cluster.block_rank()) * nt + tid;
+  if (tid == 0) bad_sh = 0;
+  __syncthreads();
+
+  // A thread's run of consecutive requests, their sums in 64 bits; lengths out
+  // of range add nothing and are reported.
+  const long long most = static_cast<long long>(a.max_pages) << shift;
+  const int per = (R + nt - 1) / nt, r0 = min(tid * per, R), r1 = min(r0 + per, R);
+  auto pages = [&](long long tokens) { return static_cast<int>((tokens + a.page_size - 1) >> shift); };
+  long long s0 = 0, s1 = 0, s2 = 0;
+  bool bad = false;
+  for (int i = r0; i < r1; ++i) {
+    const int len = a.len[i], keep = a.keep ? a.keep[i] : len, add = a.add[i];
+    const long long now = static_cast<long long>(keep) + add;
+    if (len < 0 || len > most || keep < 0 || keep > len || add < 0 || now > most) {
+      bad = true;
+      cu[i] = ct[i] = cb[i] = kp[i] = hv[i] = 0;
+      continue;
+    }
+    const int have = pages(len), want = pages(now);
+    cu[i] = add;
+    ct[i] = max(want - have, 0);
+    cb[i] = max(have - want, 0);
+    kp[i] = keep;
+    hv[i] = have;
+    s0 += cu[i];
+    s1 += ct[i];
+    s2 += cb[i];
+  }
+  const int n_free = a.n_free[0];
+  if (bad) bad_sh = 1;
+  long long x0 = s0, x1 = s1, x2 = s2;  // inclusive over the warp
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y0 = __shfl_up_sync(0xffffffffu, x0, o), y1 = __shfl_up_sync(0xffffffffu, x1, o),
+                    y2 = __shfl_up_sync(0xffffffffu, x2, o);
+    if (lane >= o) {
+      x0 += y0;
+      x1 += y1;
+      x2 += y2;
+    }
+  }
+  if (lane == 31) {
+    part[warp][0] = x0;
+    part[warp][1] = x1;
+    part[warp][2] = x2;
+  }
+  __syncthreads();
+  long long t0 = 0, t1 = 0, t2 = 0;
+  for (int w = 0; w < (nt >> 5); ++w) {
+    if (w == warp) {
+      x0 += t0;
+      x1 += t1;
+      x2 += t2;
+    }
+    t0 += part[w][0];
+    t1 += part[w][1];
+    t2 += part[w][2];
+  }
+  int status = SF_PLAN_OK;
+  if (n_free < 0 || n_free + t2 > a.free_cap || t1 > n_free + t2) status = SF_PLAN_PAGES;
+  if (t0 > a.max_rows) status = SF_PLAN_ROWS;
+  if (bad_sh) status = SF_PLAN_LENGTH;
+  const bool ok = status == SF_PLAN_OK;
+  if (ok) {  // then the sums fit 32 bits (max_rows, free_cap)
+    int e0 = static_cast<int>(x0 - s0), e1 = static_cast<int>(x1 - s1), e2 = static_cast<int>(x2 - s2);
+    for (int i = r0; i < r1; ++i) {
+      const int add = cu[i], take = ct[i], back = cb[i];
+      cu[i] = e0;
+      ct[i] = e1;
+      cb[i] = e2;
+      e0 += add;
+      e1 += take;
+      e2 += back;
+    }
+    if (tid == 0) {
+      cu[R] = static_cast<int>(t0);
+      ct[R] = static_cast<int>(t1);
+      cb[R] = static_cast<int>(t2);
+    }
+  }
+  __syncthreads();
+  const int rows = ok ? cu[R] : 0, taken = ok ? ct[R] : 0, given = ok ? cb[R] : 0;
+
+  // Pages given back, on top of the free list: request i's last cb[i+1] - cb[i].
+  for (int f = gtid; f < given; f += nthreads) {
+    const int i = owner_of(cb, R, f);
+    a.free_list[n_free + f] = a.block_table[i * a.table_stride + hv[i] - (cb[i + 1] - f)];
+  }
+  cluster.sync();
+
+  const int top = n_free + given - 1;
+  for (int i = gtid; i < R; i += nthreads) {
+    a.len_out[i] = ok ? kp[i] + (cu[i + 1] - cu[i]) : a.len[i];
+    a.cu_rows[i] = ok ? cu[i] : 0;
+  }
+  if (gtid == 0) {
+    a.cu_rows[R] = rows;
+    a.n_free_out[0] = n_free + given - taken;
+    a.status[0] = status;
+  }
+  for (int k = gtid; k < taken; k += nthreads) {
+    const int i = owner_of(ct, R, k);
+    a.block_table[i * a.table_stride + hv[i] + (k - ct[i])] = a.free_list[top - k];
+  }
+  for (int r = gtid; r < a.max_rows; r += nthreads) {
+    int slot = -1, pos = 0, req = -1;
+    if (r < rows) {
+      req = owner_of(cu, R, r);
+      pos = kp[req] + (r - cu[req]);
+      const int j = pos >> shift;
+      const int page =
+          j < hv[req] ? a.block_table[req * a.table_stride + j] : a.free_list[top - (ct[req] + j - hv[req])];
+      slot = page * a.page_size + (pos & (a.page_size - 1));
+    }
+    a.slots[r] = slot;
+    a.positions[r] = pos;
+    a.row_request[r] = req;
+  }
+}
+
+// ---- sf_paged_append ----------------------------------------------------------
+//
+// A warp per (row, head): lane l holds the pairs (i, i + d/2) for i in
+// [NP l, NP l + NP), NP = d/64, so a rotation needs no exchange, the group's
+// min and max are one butterfly, and the lanes of a code word OR their codes
+// together.  The rotation is sf_rope's (fp64, one rounding): theta^(-2i/d) is
+// taken once per block and the row's sines and cosines once per (block, row),
+// shared by the row's heads.  Bound by memory for many rows (a source value is
+// read once, 4 bits and a bf16 come out), by latency for few, when the heads
+// of a row are spread over blocks.
+
+constexpr int kAppWarps = 8;
+
+struct AppendArgs {
+  const void *k, *v, *q;
+  uint16_t *q_out, *k_val, *v_val;
+  uint32_t *k_codes, *k_param, *v_codes, *v_param;
+  const int32_t *slots, *positions;
+  int64_t k_stride, v_stride, q_stride, q_out_stride, page_rows;
+  double theta;
+  int T, Hq, Hkv, shift, slot_end;
+};
+
+template <int NP, typename S>
+__device__ __forceinline__ void load_row(const S* p, float (&x)[NP]) {
+  if constexpr (sizeof(S) == 4) {
+    if constexpr (NP == 1) {
+      x[0] = *reinterpret_cast<const float*>(p);
+    } else if constexpr (NP == 2) {
+      const float2 f = *reinterpret_cast<const float2*>(p);
+      x[0] = f.x;
+      x[1] = f.y;
+    } else {
+      const float4 f = *reinterpret_cast<const float4*>(p);
+      x[0] = f.x;
+      x[1] = f.y;
+      x[2] = f.z;
+      x[3] = f.w;
+    }
+  } else {
+    uint16_t u[NP];
+    if constexpr (NP == 1)
+      u[0] = *reinterpret_cast<const uint16_t*>(p);
+    else if constexpr (NP == 2)
+      *reinterpret_cast<uint32_t*>(u) = *reinterpret_cast<const uint32_t*>(p);
+    else
+      *reinterpret_cast<uint2*>(u) = *reinterpret_cast<const uint2*>(p);
+#pragma unroll
+    for (int j = 0; j < NP; ++j) x[j] = sfd::bf16_bits_to_float(u[j]);
+  }
+}
+
+template <int NP>
+__device__ __forceinline__ void store_bf16(uint16_t* p, const uint16_t (&u)[NP]) {
+#pragma unroll
+  for (int j = 0; j < NP; ++j) p[j] = u[j];
+}
+
+template <int D, typename S>
+__global__ void __launch_bounds__(32 * kAppWarps) paged_append_kernel(const __grid_constant__ AppendArgs A) {
+  constexpr int NP = D / 64, H = D / 2;
+  __shared__ double freq[H];
+  __shared__ double cs[H], sn[H];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const bool rot = A.theta > 0.0;
+  if (rot)
+    for (int i = tid; i < H; i += 32 * kAppWarps) freq[i] = pow(A.theta, -2.0 * i / D);
+  const int heads = 2 * A.Hkv + A.Hq;
+  for (int t = blockIdx.x; t < A.T; t += gridDim.x) {
+    const int slot = A.slots[t];
+    if (slot < 0 || slot >= A.slot_end) continue;  // the same for the whole block
+    if (rot) {
+      __syncthreads();
+      for (int i = tid; i < H; i += 32 * kAppWarps) sincos(A.positions[t] * freq[i], &sn[i], &cs[i]);
+      __syncthreads();
+    }
+    const int64_t page_row = static_cast<int64_t>(slot >> A.shift) * A.page_rows + (slot & ((1 << A.shift) - 1));
+    for (int u = blockIdx.y * kAppWarps + warp; u < heads; u += gridDim.y * kAppWarps) {
+      const int kind = u < A.Hkv ? 0 : u < 2 * A.Hkv ? 1 : 2;  // key, value, query
+      const int h = u - (kind == 0 ? 0 : kind == 1 ? A.Hkv : 2 * A.Hkv);
+      const S* src = static_cast<const S*>(kind == 0 ? A.k : kind == 1 ? A.v : A.q) +
+                     t * (kind == 0 ? A.k_stride : kind == 1 ? A.v_stride : A.q_stride) + h * D + NP * lane;
+      float lo[NP], hi[NP];
+      load_row<NP, S>(src, lo);
+      load_row<NP, S>(src + H, hi);
+      if (rot && kind != 1) {
+        double a[NP], b[NP];
+#pragma unroll
+        for (int j = 0; j < NP; ++j) {
+          const double c = cs[NP * lane + j], s = sn[NP * lane + j], x = lo[j], y = hi[j];
+          a[j] = x * c - y * s;
+          b[j] = y * c + x * s;
+        }
+        if (kind == 2) {
+          uint16_t ua[NP], ub[NP];
+#pragma unroll
+          for (int j = 0; j < NP; ++j) {
+            ua[j] = sfd::to_bf16(a[j]);
+            ub[j] = sfd::to_bf16(b[j]);
+          }
+          uint16_t* out = A.q_out + t * A.q_out_stride + h * D + NP * lane;
+          store_bf16<NP>(out, ua);
+          store_bf16<NP>(out + H, ub);
+          continue;
+        }
+#pragma unroll
+        for (int j = 0; j < NP; ++j) {
+          lo[j] = static_cast<float>(a[j]);
+          hi[j] = static_cast<float>(b[j]);
+        }
+      }
+      // 4-bit min-max quantization of the token-head
+      float mn = lo[0], mx = lo[0];
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        mn = fminf(mn, fminf(lo[j], hi[j]));
+        mx = fmaxf(mx, fmaxf(lo[j], hi[j]));
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      }
+      __half s16 = __float2half_rn(fminf(__fdiv_rn(__fsub_rn(mx, mn), 15.0f), 65504.0f));
+      if (__half2float(s16) == 0.0f) s16 = __float2half_rn(1.0f);
+      const float s = __half2float(s16);
+      const float zf = fminf(fmaxf(rintf(__fdiv_rn(-mn, s)), 0.0f), 15.0f);
+      uint32_t wl = 0, wh = 0;  // the lane's codes at their place in the word
+      uint16_t vl[NP], vh[NP];
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        const float cl = fminf(fmaxf(rintf(__fdiv_rn(lo[j], s)) + zf, 0.0f), 15.0f);
+        const float ch = fminf(fmaxf(rintf(__fdiv_rn(hi[j], s)) + zf, 0.0f), 15.0f);
+        const int at = 4 * ((NP * lane + j) & 7);
+        wl |= static_cast<uint32_t>(cl) << at;
+        wh |= static_cast<uint32_t>(ch) << at;
+        vl[j] = __bfloat16_as_ushort(__float2bfloat16_rn(s * (cl - zf)));
+        vh[j] = __bfloat16_as_ushort(__float2bfloat16_rn(s * (ch - zf)));
+      }
+#pragma unroll
+      for (int o = 1; o < 8 / NP; o <<= 1) {
+        wl |= __shfl_xor_sync(0xffffffffu, wl, o);
+        wh |= __shfl_xor_sync(0xffffffffu, wh, o);
+      }
+      const int64_t r = page_row + (static_cast<int64_t>(h) << A.shift);
+      uint32_t* codes = (kind ? A.v_codes : A.k_codes) + r * (D / 8);
+      if (lane % (8 / NP) == 0) {
+        codes[NP * lane / 8] = wl;
+        codes[H / 8 + NP * lane / 8] = wh;
+      }
+      if (lane == 0)
+        (kind ? A.v_param : A.k_param)[r] =
+            static_cast<uint32_t>(__half_as_ushort(s16)) |
+            static_cast<uint32_t>(__half_as_ushort(__int2half_rn(static_cast<int>(zf)))) << 16;
+      uint16_t* val = kind ? A.v_val : A.k_val;
+      if (val != nullptr) {
+        val += (static_cast<int64_t>(t) * A.Hkv + h) * D + NP * lane;
+        store_bf16<NP>(val, vl);
+        store_bf16<NP>(val + H, vh);
+      }
+    }
+  }
+}
+
+template <typename S>
+void launch_append(const AppendArgs& A, int d, dim3 grid, cudaStream_t s) {
+  if (d == 64)
+    paged_append_kernel<64, S><<<grid, 32 * kAppWarps, 0, s>>>(A);
+  else if (d == 128)
+    paged_append_kernel<128, S><<<grid, 32 * kAppWarps, 0, s>>>(A);
+  else
+    paged_append_kernel<256, S><<<grid, 32 * kAppWarps, 0, s>>>(A);
+}
+
+}  // namespace
+
+extern "C" sf_status sf_paged_plan(const sf_paged_plan_args* a, sf_stream_t stream) {
+  SF_REQUIRE(a, "sf_paged_plan: null arguments");
+  SF_REQUIRE(a->len && a->add && a->block_table && a->free_list && a->n_free && a->len_out && a->n_free_out &&
+                 a->cu_rows && a->slots && a->positions && a->row_request && a->status,
+             "sf_paged_plan: null pointer");
+  SF_REQUIRE(a->R >= 1 && a->R <= kPlanMaxR, "sf_paged_plan: R must be in [1, %d]", kPlanMaxR);
+  SF_REQUIRE(sf::pow2_in(a->page_size, 16, 256), "sf_paged_plan: page_size must be a power of two in [16, 256]");
+  SF_REQUIRE(a->max_pages >= 1 && static_cast<int64_t>(a->max_pages) * a->page_size < (1ll << 31),
+             "sf_paged_plan: need max_pages >= 1 and max_pages * page_size < 2^31");
+  SF_REQUIRE(a->table_stride >= a->max_pages, "sf_paged_plan: table_stride is below max_pages");
+  SF_REQUIRE(a->max_rows >= 1 && a->free_cap >= 1, "sf_paged_plan: need max_rows >= 1 and free_cap >= 1");
+  PlanArgs P{*a, sf::log2i(a->page_size)};
+  // One small block for a decode batch; eight blocks share the rows of a step
+  // that has many.
+  const bool small = a->R <= 128 && a->max_rows <= 512;
+  const int blocks = small || a->max_rows <= 4096 ? 1 : 8;
+  const size_t smem = static_cast<size_t>(kPlanArrays) * (a->R + 1) * sizeof(int);
+  if (smem > 48 * 1024)
+    SF_CHECK_CUDA(cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem)));
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(small ? 128 : 1024);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = sf::as_cuda(stream);
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = blocks;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  SF_CHECK_CUDA(cudaLaunchKernelEx(&cfg, paged_plan_kernel, P));
+  return sf::check_launch("paged_plan_kernel");
+}
+
+extern "C" sf_status sf_paged_append(const sf_paged_append_args* a, sf_stream_t stream) {
+  const char* what = "sf_paged_append";
+  SF_REQUIRE(a, "%s: null arguments", what);
+  sf_status st = sf::check_paged_kv(a->kv, what);
+  if (st != SF_OK) return st;
+  const sf_paged_kv& kv = *a->kv;
+  SF_REQUIRE(a->T >= 0, "%s: T must be >= 0", what);
+  SF_REQUIRE(a->src_type == SF_F32 || a->src_type == SF_BF16, "%s: src_type must be SF_F32 or SF_BF16", what);
+  SF_REQUIRE(a->Hq >= 0 && a->Hq <= 1024, "%s: Hq must be in [0, 1024]", what);
+  SF_REQUIRE(a->theta >= 0.0 && std::isfinite(a->theta), "%s: theta must be finite and >= 0", what);
+  SF_REQUIRE((a->q != nullptr) == (a->Hq > 0) && (a->q_out != nullptr) == (a->Hq > 0),
+             "%s: q and q_out go with Hq > 0", what);
+  SF_REQUIRE(a->theta > 0.0 || a->Hq == 0, "%s: q is only rotated: it needs theta > 0", what);
+  if (a->T == 0) return SF_OK;
+  SF_REQUIRE(a->k && a->v && a->slots, "%s: null pointer", what);
+  SF_REQUIRE(a->theta == 0.0 || a->positions, "%s: the rotation needs positions", what);
+  const int es = a->src_type == SF_F32 ? 4 : 2;
+  const int64_t kv_row = static_cast<int64_t>(kv.Hkv) * kv.d, q_row = static_cast<int64_t>(a->Hq) * kv.d;
+  SF_REQUIRE(a->k_stride >= kv_row && a->v_stride >= kv_row, "%s: k_stride and v_stride must be at least Hkv * d",
+             what);
+  SF_REQUIRE(a->Hq == 0 || (a->q_stride >= q_row && a->q_out_stride >= q_row),
+             "%s: q_stride and q_out_stride must be at least Hq * d", what);
+  auto rows16 = [](const void* p, int64_t stride, int size) {
+    return sf::aligned(p, 16) && stride * size % 16 == 0;
+  };
+  SF_REQUIRE(rows16(a->k, a->k_stride, es) && rows16(a->v, a->v_stride, es) &&
+                 (a->Hq == 0 || (rows16(a->q, a->q_stride, es) && rows16(a->q_out, a->q_out_stride, 2))),
+             "%s: rows of k, v, q and q_out must be 16-byte aligned", what);
+  SF_REQUIRE((!a->k_val || sf::aligned(a->k_val, 16)) && (!a->v_val || sf::aligned(a->v_val, 16)),
+             "%s: k_val and v_val must be 16-byte aligned", what);
+  AppendArgs A{};
+  A.k = a->k;
+  A.v = a->v;
+  A.q = a->q;
+  A.q_out = a->q_out;
+  A.k_val = a->k_val;
+  A.v_val = a->v_val;
+  A.k_codes = kv.k_codes;
+  A.k_param = kv.k_param;
+  A.v_codes = kv.v_codes;
+  A.v_param = kv.v_param;
+  A.slots = a->slots;
+  A.positions = a->positions;
+  A.k_stride = a->k_stride;
+  A.v_stride = a->v_stride;
+  A.q_stride = a->q_stride;
+  A.q_out_stride = a->q_out_stride;
+  A.page_rows = sf::page_rows(&kv);
+  A.theta = a->theta;
+  A.T = a->T;
+  A.Hq = a->Hq;
+  A.Hkv = kv.Hkv;
+  A.shift = sf::log2i(kv.page_size);
+  A.slot_end = kv.num_pages * kv.page_size;
+  // Few rows: a row's heads are spread over blocks until the SMs are filled.
+  // Many rows: a block keeps all heads of its rows and loops over rows.
+  const int sms = sf::sm_count();
+  const int need = (2 * kv.Hkv + a->Hq + kAppWarps - 1) / kAppWarps;  // blocks that one row can fill
+  const int gx = std::min(a->T, sms * 8);
+  const int gy = std::max(1, std::min(need, sms * 2 / gx));
+  if (a->src_type == SF_F32)
+    launch_append<float>(A, kv.d, dim3(gx, gy), sf::as_cuda(stream));
+  else
+    launch_append<uint16_t>(A, kv.d, dim3(gx, gy), sf::as_cuda(stream));
+  return sf::check_launch("paged_append_kernel");
+}
