@@ -319,9 +319,9 @@ class _Case:
         torch.cuda.synchronize()
         return out
 
-    def check(self, sf, out_type=torch.float32, **kw):
-        out = _f64(self.run(sf, out_type, **kw))
-        q = _f64(self.q)
+    def check(self, sf, out_type=torch.float32, out=None, **kw):
+        out = _f64(self.run(sf, out_type, **kw) if out is None else out)
+        q = _f64(self.q)[:len(out)]
         want = osv.attention(q, self.val[0], self.val[1], self.cu, self.lens, self.table, out=np.full(q.shape, 7.0),
                              **kw)
         scale = kw.get("scale") or 1.0 / np.sqrt(q.shape[-1])
@@ -457,10 +457,9 @@ def test_attention_strides_and_layers(sf):
 def test_attention_rows_behind_the_buffer(sf):
     """cu_rows past T, and lengths outside the table: clamped, never read or written out of bounds."""
     c = _Case(sf, 41, [1, 3], [60, 90], 4, 2, 128, 16, extra_rows=0)
-    want = c.run(sf)
     out = torch.full((2, 4, 128), 7.0, device="cuda")
     sf.attn_paged(c.q[:2].cuda(), c.kv, _i32(c.cu), _i32(c.lens), _i32(c.table), out)
-    assert torch.equal(out, want[:2])
+    c.check(sf, out=out)      # to rounding: fewer columns are other runs of stages, whose sums come in another order
     out = c.run(sf)
     c.lens = [-5, 10 ** 9]
     got = c.run(sf)                                       # request 0 has no token, request 1 all that its table holds
