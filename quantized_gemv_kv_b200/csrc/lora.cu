@@ -12,7 +12,10 @@
 //    distributed shared memory, both in a fixed order;
 //  * out = y + h B^T: the blocks split N.  h enters as three bf16 terms (24
 //    bits), so the second product keeps fp32 accuracy: h is fp32, and its
-//    rounding to bf16 would show in the fp32 output.
+//    rounding to bf16 would show in the fp32 output.  Which column of a group of
+//    32 a product's column stands for, and which rank a step's, is free too: so
+//    that a lane's outputs and its ranks of a B row are 16 contiguous bytes (half
+//    the memory instructions of the plain order; they were what bound it).
 // What the second product reads does not wait for the first: a warp's first B
 // is loaded, and y prefetched to L2, before h is summed.  Bound by latency for
 // a decode batch (a chain of two weight reads and a cluster barrier), by the
@@ -32,7 +35,7 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxWindow = 64;
 constexpr int kRows = 16;  // rows worked on at a time
-constexpr int kNB = 4;     // tiles of 8 outputs that a warp takes at a time
+constexpr int kNB = 4;     // tiles of 8 outputs that a warp takes at a time: a group of 32 columns
 
 __device__ __forceinline__ void bmma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                      uint32_t b1) {
@@ -46,7 +49,7 @@ struct LoraArgs {
   int window;  // rows of a window
   int share;   // clusters per window
   int log_blocks;
-  int vec;  // rows of y and out allow 8-byte accesses
+  int vec;  // rows of y and out allow 16-byte accesses
 };
 
 // KS: steps of 16 ranks that the second product takes (rank <= 16 KS, zeros beyond it).
@@ -92,10 +95,10 @@ __device__ void lora_rows(const LoraArgs& P, Shared<KS>& S, const int* list, int
   const int blocks = 1 << P.log_blocks, block = static_cast<int>(cluster.block_rank());
   const float scale = a.scale[id];
 
-  // this block's run of 8-column output tiles
-  const uint32_t tiles = (a.N + 7u) / 8u;
-  const int t0 = static_cast<int>(static_cast<uint64_t>(tiles) * block >> P.log_blocks);
-  const int t1 = static_cast<int>(static_cast<uint64_t>(tiles) * (block + 1) >> P.log_blocks);
+  // this block's run of groups of 32 output columns
+  const uint32_t groups = (a.N + 31u) / 32u;
+  const int g0 = static_cast<int>(static_cast<uint64_t>(groups) * block >> P.log_blocks);
+  const int g1 = static_cast<int>(static_cast<uint64_t>(groups) * (block + 1) >> P.log_blocks);
   const int r[2] = {g, g + 8};
   const uint16_t* x[2];
   const float* y[2];
@@ -104,29 +107,39 @@ __device__ void lora_rows(const LoraArgs& P, Shared<KS>& S, const int* list, int
   for (int z = 0; z < 2; ++z) {
     const int64_t row = row0 + list[r[z] < n ? r[z] : 0];
     x[z] = a.x + row * a.x_stride + 8 * t;
-    y[z] = a.y ? a.y + row * a.y_stride + 2 * t : nullptr;
-    out[z] = a.out + row * a.out_stride + 2 * t;
+    y[z] = a.y ? a.y + row * a.y_stride + 4 * t : nullptr;
+    out[z] = a.out + row * a.out_stride + 4 * t;
   }
-  const uint16_t* const Bw = a.B + (static_cast<int64_t>(id) * a.N + g) * a.rank + 4 * t;
+  // Column n of tile j is column 16 (j/2) + 4 (n/2) + 2 (j%2) + n%2 of the group, so that lane t's are 4 t .. 4 t + 3
+  // and 16 more.  Rank i of step q is, for lane t's four, 32 (q/2) + 8 t + 4 (q%2) + i (rank <= 16: 4 t + i).
+  const int bcol = 4 * (g >> 1) + (g & 1);
+  const uint16_t* const Bw = a.B + (static_cast<int64_t>(id) * a.N + bcol) * a.rank + (KS == 1 ? 4 : 8) * t;
   uint2 b[C::KB][kNB];
-  auto load_b = [&](int tile, int q0) {
-    const uint16_t* from = Bw + static_cast<int64_t>(8 * tile) * a.rank + 16 * q0;
-    const int cols = min(t1 - tile, kNB);  // tiles there are
+  auto load_b = [&](int group, int q0) {
+    const uint16_t* from = Bw + static_cast<int64_t>(32 * group) * a.rank + 16 * q0;
 #pragma unroll
     for (int j = 0; j < kNB; ++j) {
-      const bool in = j < cols && 8 * (tile + j) + g < a.N;
+      const int c = 16 * (j >> 1) + 2 * (j & 1);
+      const bool in = 32 * group + bcol + c < a.N;
+      if constexpr (KS == 1) {
+        b[0][j] = in && 4 * t < a.rank ? *reinterpret_cast<const uint2*>(from + c * a.rank) : make_uint2(0, 0);
+      } else {
 #pragma unroll
-      for (int q = 0; q < C::KB; ++q)
-        b[q][j] = in && 16 * (q0 + q) + 4 * t < a.rank
-                      ? *reinterpret_cast<const uint2*>(from + (8 * j) * a.rank + 16 * q)
-                      : make_uint2(0, 0);
+        for (int q = 0; q < C::KB; q += 2) {
+          const uint4 v = in && 16 * (q0 + q) + 8 * t < a.rank
+                              ? *reinterpret_cast<const uint4*>(from + c * a.rank + 16 * q)
+                              : make_uint4(0, 0, 0, 0);
+          b[q][j] = make_uint2(v.x, v.y);
+          b[q + 1][j] = make_uint2(v.z, v.w);
+        }
+      }
     }
   };
-  load_b(t0 + warp * kNB, 0);
+  if (g0 + warp < g1) load_b(g0 + warp, 0);
   if (a.y) {  // y's lines of this block, spread over the warps
-    const int c0 = 8 * t0, c1 = min(8 * t1, a.N);
+    const int c1 = min(32 * g1, a.N);
     for (int q = warp; q < n; q += kWarps)
-      for (int c = c0 + 32 * lane; c < c1; c += 1024)
+      for (int c = 32 * (g0 + lane); c < c1; c += 1024)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(a.y + static_cast<int64_t>(row0 + list[q]) * a.y_stride + c));
   }
 
@@ -193,23 +206,23 @@ __device__ void lora_rows(const LoraArgs& P, Shared<KS>& S, const int* list, int
   cluster.barrier_arrive();
   __syncthreads();
 
-  for (int tile = t0 + warp * kNB; tile < t1; tile += kWarps * kNB) {
-    const bool full = P.vec && tile + kNB <= t1 && 8 * (tile + kNB) <= a.N;
-    float2 v[2][kNB] = {};
+  for (int group = g0 + warp; group < g1; group += kWarps) {
+    const bool full = P.vec && 32 * (group + 1) <= a.N;
+    const int left = a.N - 32 * group - 4 * t;  // columns from the lane's first on
+    float v[2][2][4] = {};                      // rows x halves of the group
     if (a.y) {
 #pragma unroll
       for (int z = 0; z < 2; ++z)
         if (r[z] < n) {
-          const float* from = y[z] + 8 * tile;
-          if (full) {
+          const float* from = y[z] + 32 * group;
 #pragma unroll
-            for (int j = 0; j < kNB; ++j) v[z][j] = *reinterpret_cast<const float2*>(from + 8 * j);
-          } else {
+          for (int h = 0; h < 2; ++h) {
+            if (full) {
+              *reinterpret_cast<float4*>(v[z][h]) = *reinterpret_cast<const float4*>(from + 16 * h);
+            } else {
 #pragma unroll
-            for (int j = 0; j < kNB; ++j) {
-              if (tile + j >= t1) continue;
-              if (8 * (tile + j) + 2 * t < a.N) v[z][j].x = from[8 * j];
-              if (8 * (tile + j) + 2 * t + 1 < a.N) v[z][j].y = from[8 * j + 1];
+              for (int i = 0; i < 4; ++i)
+                if (16 * h + i < left) v[z][h][i] = from[16 * h + i];
             }
           }
         }
@@ -221,29 +234,33 @@ __device__ void lora_rows(const LoraArgs& P, Shared<KS>& S, const int* list, int
       for (int q = 0; q < C::KB; ++q)
 #pragma unroll
         for (int z = 2; z >= 0; --z) {  // the small terms first
-          const uint16_t* from = &S.term[z][g][16 * (q0 + q) + 4 * t];
+          const uint16_t* from =
+              &S.term[z][g][KS == 1 ? 4 * t : 16 * (q0 + (q & ~1)) + 8 * t + 4 * (q & 1)];
           const uint2 lo = *reinterpret_cast<const uint2*>(from);
           const uint2 hi = *reinterpret_cast<const uint2*>(from + 8 * C::PITCH);
 #pragma unroll
           for (int j = 0; j < kNB; ++j) bmma(d[j], lo.x, hi.x, lo.y, hi.y, b[q][j].x, b[q][j].y);
         }
       if (q0 + C::KB < KS)
-        load_b(tile, q0 + C::KB);
-      else if (tile + kWarps * kNB < t1)
-        load_b(tile + kWarps * kNB, 0);
+        load_b(group, q0 + C::KB);
+      else if (group + kWarps < g1)
+        load_b(group + kWarps, 0);
     }
 #pragma unroll
     for (int z = 0; z < 2; ++z)
       if (r[z] < n) {
-        float* to = out[z] + 8 * tile;
+        float* to = out[z] + 32 * group;
 #pragma unroll
-        for (int j = 0; j < kNB; ++j) {
-          const float2 s = make_float2(v[z][j].x + d[j][2 * z], v[z][j].y + d[j][2 * z + 1]);
+        for (int h = 0; h < 2; ++h) {
+          float o[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[i] = v[z][h][i] + d[2 * h + (i >> 1)][2 * z + (i & 1)];
           if (full) {
-            *reinterpret_cast<float2*>(to + 8 * j) = s;
-          } else if (tile + j < t1) {
-            if (8 * (tile + j) + 2 * t < a.N) to[8 * j] = s.x;
-            if (8 * (tile + j) + 2 * t + 1 < a.N) to[8 * j + 1] = s.y;
+            *reinterpret_cast<float4*>(to + 16 * h) = make_float4(o[0], o[1], o[2], o[3]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (16 * h + i < left) to[16 * h + i] = o[i];
           }
         }
       }
@@ -296,19 +313,40 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const __grid_constant
     }
   }
 
-  // Rows without an adapter, spread over the window's clusters, four at a time.
-  if (a.out != a.y) {
-    const int c0 = static_cast<int>(static_cast<int64_t>(a.N) * block >> P.log_blocks);
-    const int c1 = static_cast<int>(static_cast<int64_t>(a.N) * (block + 1) >> P.log_blocks);
-    for (int q = 4 * turn; q < S.bare_n; q += 4 * P.share)
-      for (int c = c0 + tid; c < c1; c += kThreads) {
-        float v[4] = {};
+  // Rows without an adapter, spread over the window's clusters: four columns, eight rows on their way at once.
+  if (a.out != a.y && S.bare_n > turn) {
+    const int p0 = static_cast<int>(static_cast<int64_t>((a.N + 3) / 4) * block >> P.log_blocks);
+    const int p1 = static_cast<int>(static_cast<int64_t>((a.N + 3) / 4) * (block + 1) >> P.log_blocks);
+    const int mine = (S.bare_n - 1 - turn) / P.share + 1;  // rows turn, turn + share, ...
+    constexpr int kAhead = 8;
+    for (int c = 4 * (p0 + tid); c < 4 * p1; c += 4 * kThreads)
+      for (int q = 0; q < mine; q += kAhead) {
+        const bool full = P.vec && c + 4 <= a.N;
+        float v[kAhead][4] = {};
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (a.y && q + k < S.bare_n) v[k] = a.y[static_cast<int64_t>(row0 + S.bare[q + k]) * a.y_stride + c];
+        for (int k = 0; k < kAhead; ++k) {
+          if (!a.y || q + k >= mine) continue;
+          const float* from = a.y + static_cast<int64_t>(row0 + S.bare[turn + (q + k) * P.share]) * a.y_stride + c;
+          if (full) {
+            *reinterpret_cast<float4*>(v[k]) = *reinterpret_cast<const float4*>(from);
+          } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (q + k < S.bare_n) a.out[static_cast<int64_t>(row0 + S.bare[q + k]) * a.out_stride + c] = v[k];
+            for (int i = 0; i < 4; ++i)
+              if (c + i < a.N) v[k][i] = from[i];
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          if (q + k >= mine) continue;
+          float* to = a.out + static_cast<int64_t>(row0 + S.bare[turn + (q + k) * P.share]) * a.out_stride + c;
+          if (full) {
+            *reinterpret_cast<float4*>(to) = make_float4(v[k][0], v[k][1], v[k][2], v[k][3]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (c + i < a.N) to[i] = v[k][i];
+          }
+        }
       }
   }
   if (again) cluster.barrier_wait();  // the other blocks have read this one's sums
@@ -353,8 +391,7 @@ extern "C" sf_status sf_lora_add(const sf_lora_args* a, sf_stream_t stream) {
              "%s: A, B and the rows of x must be 16-byte aligned", what);
   LoraArgs P{};
   P.a = *a;
-  P.vec = a->N % 2 == 0 && sf::aligned(a->out, 8) && a->out_stride % 2 == 0 &&
-          (!a->y || (sf::aligned(a->y, 8) && a->y_stride % 2 == 0));
+  P.vec = sf::aligned(a->out, 16) && a->out_stride % 4 == 0 && (!a->y || (sf::aligned(a->y, 16) && a->y_stride % 4 == 0));
   // Rows of one adapter are found within a window: wide windows for a decode batch, where the adapters' weights are
   // what is read, narrow ones for prompts, where more of them run at once.
   P.window = a->T <= 128 ? kMaxWindow : kRows;
