@@ -31,6 +31,8 @@ constexpr int kPlanMaxR = 8192;
 struct PlanArgs {
   sf_paged_plan_args a;
   int shift;  // log2(page_size)
+  int vec;    // the rows' outputs allow 16-byte stores
+  int own;    // rows a thread takes at a time: 1 or 4
 };
 
 // Index of the last entry of ascending cum[0..R] that is <= v (cum[0] = 0,
@@ -168,19 +170,36 @@ __global__ void __launch_bounds__(1024) paged_plan_kernel(const __grid_constant_
     const int i = owner_of(ct, R, k);
     a.block_table[i * a.table_stride + hv[i] + (k - ct[i])] = a.free_list[top - k];
   }
-  for (int r = gtid; r < a.max_rows; r += nthreads) {
-    int slot = -1, pos = 0, req = -1;
-    if (r < rows) {
-      req = owner_of(cu, R, r);
-      pos = kp[req] + (r - cu[req]);
-      const int j = pos >> shift;
-      const int page =
-          j < hv[req] ? a.block_table[req * a.table_stride + j] : a.free_list[top - (ct[req] + j - hv[req])];
-      slot = page * a.page_size + (pos & (a.page_size - 1));
+  // Rows: with many, four consecutive ones a thread (one search, then a walk).
+  const int own = P.own;
+  for (int r0 = own * gtid; r0 < a.max_rows; r0 += own * nthreads) {
+    int slot[4], pos[4], req[4];
+    int i = r0 < rows ? owner_of(cu, R, r0) : 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      slot[k] = req[k] = -1;
+      pos[k] = 0;
+      if (k >= own || r0 + k >= rows) continue;
+      while (cu[i + 1] <= r0 + k) ++i;
+      req[k] = i;
+      pos[k] = kp[i] + (r0 + k - cu[i]);
+      const int j = pos[k] >> shift;
+      const int page = j < hv[i] ? a.block_table[i * a.table_stride + j] : a.free_list[top - (ct[i] + j - hv[i])];
+      slot[k] = page * a.page_size + (pos[k] & (a.page_size - 1));
     }
-    a.slots[r] = slot;
-    a.positions[r] = pos;
-    a.row_request[r] = req;
+    if (P.vec && own == 4 && r0 + 4 <= a.max_rows) {
+      *reinterpret_cast<int4*>(a.slots + r0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+      *reinterpret_cast<int4*>(a.positions + r0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+      *reinterpret_cast<int4*>(a.row_request + r0) = make_int4(req[0], req[1], req[2], req[3]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (k < own && r0 + k < a.max_rows) {
+          a.slots[r0 + k] = slot[k];
+          a.positions[r0 + k] = pos[k];
+          a.row_request[r0 + k] = req[k];
+        }
+    }
   }
 }
 
@@ -188,14 +207,25 @@ __global__ void __launch_bounds__(1024) paged_plan_kernel(const __grid_constant_
 //
 // A warp per (row, head): lane l holds the pairs (i, i + d/2) for i in
 // [NP l, NP l + NP), NP = d/64, so a rotation needs no exchange, the group's
-// min and max are one butterfly, and the lanes of a code word OR their codes
-// together.  The rotation is sf_rope's (fp64, one rounding): theta^(-2i/d) is
-// taken once per block and the row's sines and cosines once per (block, row),
-// shared by the row's heads.  Bound by memory for many rows (a source value is
-// read once, 4 bits and a bf16 come out), by latency for few, when the heads
-// of a row are spread over blocks.
+// min and max are one warp reduction each, and the lanes of a code word OR
+// their codes together.  theta^(-2i/d) is taken once per block, the sines and
+// cosines of a group of rows once per block by all its threads, shared by the
+// rows' heads.
+//
+// Every result is the fp64 or IEEE one rounded once, as sf_rope and
+// sf_kv_append have it, but computed in fp32 where that cannot differ:
+//  * a query is rotated in fp32 and both ends of its error interval rounded to
+//    bf16; only where they differ (one in some thousands) fp64 decides.  The
+//    conversions to and from fp64 of every query bound the kernel before;
+//  * a code is rint(x / s): x times a reciprocal, unless that lies within 2^-16
+//    of a half, where the division decides.
+// Bound by memory for many rows (a source value is read once, 4 bits and a bf16
+// come out), so a warp has the sources of the next kAhead rows of a head on
+// their way; by latency for few rows, when a row's heads are spread over
+// blocks.
 
 constexpr int kAppWarps = 8;
+constexpr int kAhead = 4;
 
 struct AppendArgs {
   const void *k, *v, *q;
@@ -205,6 +235,7 @@ struct AppendArgs {
   int64_t k_stride, v_stride, q_stride, q_out_stride, page_rows;
   double theta;
   int T, Hq, Hkv, shift, slot_end;
+  int group;  // rows that a block takes at a time
 };
 
 template <int NP, typename S>
@@ -238,111 +269,182 @@ __device__ __forceinline__ void load_row(const S* p, float (&x)[NP]) {
 
 template <int NP>
 __device__ __forceinline__ void store_bf16(uint16_t* p, const uint16_t (&u)[NP]) {
-#pragma unroll
-  for (int j = 0; j < NP; ++j) p[j] = u[j];
+  if constexpr (NP == 1)
+    p[0] = u[0];
+  else if constexpr (NP == 2)
+    *reinterpret_cast<uint32_t*>(p) = u[0] | static_cast<uint32_t>(u[1]) << 16;
+  else
+    *reinterpret_cast<uint2*>(p) =
+        make_uint2(u[0] | static_cast<uint32_t>(u[1]) << 16, u[2] | static_cast<uint32_t>(u[3]) << 16);
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+  float m;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+  return m;
+}
+__device__ __forceinline__ float warp_min(float v) {
+  float m;
+  asm("redux.sync.min.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+  return m;
+}
+
+// bf16(a c + b s) rounded once; c and s are fp64, ch and sh their fp32 values.
+// In fp32, u = a ch and v = b sh are off by at most 2^-24 |.| each for ch and
+// the product, their sum by 2^-24 of itself: within 2^-22 (|u| + |v|).
+__device__ __forceinline__ uint16_t rotated_bf16(float a, float b, float ch, float sh, const double2* cs, bool second) {
+  const float u = a * ch, r = fmaf(b, sh, u), e = 0x1p-22f * (fabsf(u) + fabsf(b * sh)) + 1e-40f;
+  const uint16_t lo = __bfloat16_as_ushort(__float2bfloat16_rn(r - e));
+  const uint16_t hi = __bfloat16_as_ushort(__float2bfloat16_rn(r + e));
+  if (lo == hi) return lo;
+  const double c = cs->x, s = second ? cs->y : -cs->y;
+  return sfd::to_bf16(static_cast<double>(a) * c + static_cast<double>(b) * s);
+}
+
+// clamp(rint(x / s) + z, 0, 15) with the division and rint of IEEE, as a float.
+__device__ __forceinline__ float code_of(float x, float s, float inv, float z) {
+  float r = fminf(fmaxf(x * inv, -32.f), 32.f);  // beyond, the clamp decides
+  float n = (r + 12582912.f) - 12582912.f;       // rint
+  if (fabsf(fabsf(r - n) - 0.5f) < 0x1p-16f) n = rintf(__fdiv_rn(x, s));
+  return fminf(fmaxf(n + z, 0.f), 15.f);
 }
 
 template <int D, typename S>
 __global__ void __launch_bounds__(32 * kAppWarps) paged_append_kernel(const __grid_constant__ AppendArgs A) {
-  constexpr int NP = D / 64, H = D / 2;
+  constexpr int NP = D / 64, H = D / 2, MAX_ROWS = 32 * kAppWarps / H;
   __shared__ double freq[H];
-  __shared__ double cs[H], sn[H];
+  __shared__ double2 turn[2][MAX_ROWS][H];  // cosine, sine; two groups, so that one barrier a group does
+  __shared__ float2 turn32[2][MAX_ROWS][H];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool rot = A.theta > 0.0;
-  if (rot)
-    for (int i = tid; i < H; i += 32 * kAppWarps) freq[i] = pow(A.theta, -2.0 * i / D);
-  const int heads = 2 * A.Hkv + A.Hq;
-  for (int t = blockIdx.x; t < A.T; t += gridDim.x) {
-    const int slot = A.slots[t];
-    if (slot < 0 || slot >= A.slot_end) continue;  // the same for the whole block
+  if (rot && tid < H) freq[tid] = pow(A.theta, -2.0 * tid / D);
+  __syncthreads();
+  const int heads = 2 * A.Hkv + A.Hq, step = gridDim.y * kAppWarps;
+  int buf = 0;
+  for (int row0 = blockIdx.x * A.group; row0 < A.T; row0 += gridDim.x * A.group, buf ^= 1) {
+    const int rows = min(A.group, A.T - row0);
+    float next_lo[kAhead][NP], next_hi[kAhead][NP];
+    int next_slot[kAhead];
+    auto load = [&](int head, int k0) {  // rows k0 .. of the group: keys, values, queries
+      const bool key = head < A.Hkv, value = !key && head < 2 * A.Hkv;
+      const int64_t stride = key ? A.k_stride : value ? A.v_stride : A.q_stride;
+      const S* src = static_cast<const S*>(key ? A.k : value ? A.v : A.q) + (row0 + k0) * stride +
+                     (head - (key ? 0 : value ? A.Hkv : 2 * A.Hkv)) * D + NP * lane;
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        next_slot[k] = -1;
+        if (k0 + k >= rows) continue;
+        next_slot[k] = A.slots[row0 + k0 + k];
+        load_row<NP, S>(src + k * stride, next_lo[k]);
+        load_row<NP, S>(src + k * stride + H, next_hi[k]);
+      }
+    };
+    int head = blockIdx.y * kAppWarps + warp, k0 = 0;
+    if (head < heads) load(head, 0);
     if (rot) {
-      __syncthreads();
-      for (int i = tid; i < H; i += 32 * kAppWarps) sincos(A.positions[t] * freq[i], &sn[i], &cs[i]);
+      if (tid < rows * H) {
+        double s, c;
+        sincos(A.positions[row0 + tid / H] * freq[tid % H], &s, &c);
+        turn[buf][tid / H][tid % H] = make_double2(c, s);
+        turn32[buf][tid / H][tid % H] = make_float2(static_cast<float>(c), static_cast<float>(s));
+      }
       __syncthreads();
     }
-    const int64_t page_row = static_cast<int64_t>(slot >> A.shift) * A.page_rows + (slot & ((1 << A.shift) - 1));
-    for (int u = blockIdx.y * kAppWarps + warp; u < heads; u += gridDim.y * kAppWarps) {
-      const int kind = u < A.Hkv ? 0 : u < 2 * A.Hkv ? 1 : 2;  // key, value, query
-      const int h = u - (kind == 0 ? 0 : kind == 1 ? A.Hkv : 2 * A.Hkv);
-      const S* src = static_cast<const S*>(kind == 0 ? A.k : kind == 1 ? A.v : A.q) +
-                     t * (kind == 0 ? A.k_stride : kind == 1 ? A.v_stride : A.q_stride) + h * D + NP * lane;
-      float lo[NP], hi[NP];
-      load_row<NP, S>(src, lo);
-      load_row<NP, S>(src + H, hi);
-      if (rot && kind != 1) {
-        double a[NP], b[NP];
+    while (head < heads) {
+      float lo[kAhead][NP], hi[kAhead][NP];
+      int slots[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        slots[k] = next_slot[k];
 #pragma unroll
         for (int j = 0; j < NP; ++j) {
-          const double c = cs[NP * lane + j], s = sn[NP * lane + j], x = lo[j], y = hi[j];
-          a[j] = x * c - y * s;
-          b[j] = y * c + x * s;
+          lo[k][j] = next_lo[k][j];
+          hi[k][j] = next_hi[k][j];
         }
+      }
+      const int kind = head < A.Hkv ? 0 : head < 2 * A.Hkv ? 1 : 2;  // key, value, query
+      const int h = head - kind * A.Hkv, row_k = k0;
+      k0 += kAhead;
+      if (k0 >= rows) {
+        k0 = 0;
+        head += step;
+      }
+      if (head < heads) load(head, k0);
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int slot = slots[k], row = row_k + k;
+        if (slot < 0 || slot >= A.slot_end) continue;  // the same for the whole warp
+        const int64_t t = row0 + row;
         if (kind == 2) {
           uint16_t ua[NP], ub[NP];
 #pragma unroll
           for (int j = 0; j < NP; ++j) {
-            ua[j] = sfd::to_bf16(a[j]);
-            ub[j] = sfd::to_bf16(b[j]);
+            const int i = NP * lane + j;
+            const float2 cs = turn32[buf][row][i];
+            ua[j] = rotated_bf16(lo[k][j], hi[k][j], cs.x, -cs.y, &turn[buf][row][i], false);
+            ub[j] = rotated_bf16(hi[k][j], lo[k][j], cs.x, cs.y, &turn[buf][row][i], true);
           }
           uint16_t* out = A.q_out + t * A.q_out_stride + h * D + NP * lane;
           store_bf16<NP>(out, ua);
           store_bf16<NP>(out + H, ub);
           continue;
         }
+        if (rot && kind == 0) {
+#pragma unroll
+          for (int j = 0; j < NP; ++j) {
+            const double2 cs = turn[buf][row][NP * lane + j];
+            const double x = lo[k][j], y = hi[k][j];
+            lo[k][j] = static_cast<float>(x * cs.x - y * cs.y);
+            hi[k][j] = static_cast<float>(y * cs.x + x * cs.y);
+          }
+        }
+        // 4-bit min-max quantization of the token-head
+        float mn = fminf(lo[k][0], hi[k][0]), mx = fmaxf(lo[k][0], hi[k][0]);
+#pragma unroll
+        for (int j = 1; j < NP; ++j) {
+          mn = fminf(mn, fminf(lo[k][j], hi[k][j]));
+          mx = fmaxf(mx, fmaxf(lo[k][j], hi[k][j]));
+        }
+        mn = warp_min(mn);
+        mx = warp_max(mx);
+        __half s16 = __float2half_rn(fminf(__fdiv_rn(__fsub_rn(mx, mn), 15.0f), 65504.0f));
+        if (__half2float(s16) == 0.0f) s16 = __float2half_rn(1.0f);
+        const float s = __half2float(s16), inv = __frcp_rn(s);
+        const float zf = code_of(-mn, s, inv, 0.f);
+        uint32_t wl = 0, wh = 0;  // the lane's codes at their place in the word
+        uint16_t vl[NP], vh[NP];
 #pragma unroll
         for (int j = 0; j < NP; ++j) {
-          lo[j] = static_cast<float>(a[j]);
-          hi[j] = static_cast<float>(b[j]);
+          const float cl = code_of(lo[k][j], s, inv, zf), ch = code_of(hi[k][j], s, inv, zf);
+          wl |= (__float_as_uint(cl + 8388608.f) & 15u) << (4 * j);
+          wh |= (__float_as_uint(ch + 8388608.f) & 15u) << (4 * j);
+          vl[j] = __bfloat16_as_ushort(__float2bfloat16_rn(s * (cl - zf)));
+          vh[j] = __bfloat16_as_ushort(__float2bfloat16_rn(s * (ch - zf)));
         }
-      }
-      // 4-bit min-max quantization of the token-head
-      float mn = lo[0], mx = lo[0];
+        const int at = 4 * (NP * lane & 7);
+        wl <<= at;
+        wh <<= at;
 #pragma unroll
-      for (int j = 0; j < NP; ++j) {
-        mn = fminf(mn, fminf(lo[j], hi[j]));
-        mx = fmaxf(mx, fmaxf(lo[j], hi[j]));
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      }
-      __half s16 = __float2half_rn(fminf(__fdiv_rn(__fsub_rn(mx, mn), 15.0f), 65504.0f));
-      if (__half2float(s16) == 0.0f) s16 = __float2half_rn(1.0f);
-      const float s = __half2float(s16);
-      const float zf = fminf(fmaxf(rintf(__fdiv_rn(-mn, s)), 0.0f), 15.0f);
-      uint32_t wl = 0, wh = 0;  // the lane's codes at their place in the word
-      uint16_t vl[NP], vh[NP];
-#pragma unroll
-      for (int j = 0; j < NP; ++j) {
-        const float cl = fminf(fmaxf(rintf(__fdiv_rn(lo[j], s)) + zf, 0.0f), 15.0f);
-        const float ch = fminf(fmaxf(rintf(__fdiv_rn(hi[j], s)) + zf, 0.0f), 15.0f);
-        const int at = 4 * ((NP * lane + j) & 7);
-        wl |= static_cast<uint32_t>(cl) << at;
-        wh |= static_cast<uint32_t>(ch) << at;
-        vl[j] = __bfloat16_as_ushort(__float2bfloat16_rn(s * (cl - zf)));
-        vh[j] = __bfloat16_as_ushort(__float2bfloat16_rn(s * (ch - zf)));
-      }
-#pragma unroll
-      for (int o = 1; o < 8 / NP; o <<= 1) {
-        wl |= __shfl_xor_sync(0xffffffffu, wl, o);
-        wh |= __shfl_xor_sync(0xffffffffu, wh, o);
-      }
-      const int64_t r = page_row + (static_cast<int64_t>(h) << A.shift);
-      uint32_t* codes = (kind ? A.v_codes : A.k_codes) + r * (D / 8);
-      if (lane % (8 / NP) == 0) {
-        codes[NP * lane / 8] = wl;
-        codes[H / 8 + NP * lane / 8] = wh;
-      }
-      if (lane == 0)
-        (kind ? A.v_param : A.k_param)[r] =
-            static_cast<uint32_t>(__half_as_ushort(s16)) |
-            static_cast<uint32_t>(__half_as_ushort(__int2half_rn(static_cast<int>(zf)))) << 16;
-      uint16_t* val = kind ? A.v_val : A.k_val;
-      if (val != nullptr) {
-        val += (static_cast<int64_t>(t) * A.Hkv + h) * D + NP * lane;
-        store_bf16<NP>(val, vl);
-        store_bf16<NP>(val + H, vh);
+        for (int o = 1; o < 8 / NP; o <<= 1) {
+          wl |= __shfl_xor_sync(0xffffffffu, wl, o);
+          wh |= __shfl_xor_sync(0xffffffffu, wh, o);
+        }
+        const int64_t r = (slot >> A.shift) * A.page_rows + (h << A.shift) + (slot & ((1 << A.shift) - 1));
+        uint32_t* codes = (kind ? A.v_codes : A.k_codes) + r * (D / 8);
+        if (lane % (8 / NP) == 0) {
+          codes[NP * lane / 8] = wl;
+          codes[H / 8 + NP * lane / 8] = wh;
+        }
+        if (lane == 0)
+          (kind ? A.v_param : A.k_param)[r] =
+              static_cast<uint32_t>(__half_as_ushort(s16)) |
+              static_cast<uint32_t>(__half_as_ushort(__float2half_rn(zf))) << 16;
+        uint16_t* val = kind ? A.v_val : A.k_val;
+        if (val != nullptr) {
+          val += (t * A.Hkv + h) * D + NP * lane;
+          store_bf16<NP>(val, vl);
+          store_bf16<NP>(val + H, vh);
+        }
       }
     }
   }
@@ -371,7 +473,9 @@ extern "C" sf_status sf_paged_plan(const sf_paged_plan_args* a, sf_stream_t stre
              "sf_paged_plan: need max_pages >= 1 and max_pages * page_size < 2^31");
   SF_REQUIRE(a->table_stride >= a->max_pages, "sf_paged_plan: table_stride is below max_pages");
   SF_REQUIRE(a->max_rows >= 1 && a->free_cap >= 1, "sf_paged_plan: need max_rows >= 1 and free_cap >= 1");
-  PlanArgs P{*a, sf::log2i(a->page_size)};
+  PlanArgs P{*a, sf::log2i(a->page_size),
+             sf::aligned(a->slots, 16) && sf::aligned(a->positions, 16) && sf::aligned(a->row_request, 16),
+             a->max_rows > 4096 ? 4 : 1};
   // One small block for a decode batch; eight blocks share the rows of a step
   // that has many.
   const bool small = a->R <= 128 && a->max_rows <= 512;
@@ -449,11 +553,12 @@ extern "C" sf_status sf_paged_append(const sf_paged_append_args* a, sf_stream_t 
   A.Hkv = kv.Hkv;
   A.shift = sf::log2i(kv.page_size);
   A.slot_end = kv.num_pages * kv.page_size;
-  // Few rows: a row's heads are spread over blocks until the SMs are filled.
-  // Many rows: a block keeps all heads of its rows and loops over rows.
-  const int sms = sf::sm_count();
+  // Few rows: a row's heads are spread over blocks until the SMs are filled.  Many rows: a block keeps all heads of a
+  // group of rows (as many as its threads have sines for) and loops over groups.
+  const int sms = sf::sm_count(), most = 64 * kAppWarps / kv.d;
+  A.group = a->T >= 4 * sms * most ? most : 1;
   const int need = (2 * kv.Hkv + a->Hq + kAppWarps - 1) / kAppWarps;  // blocks that one row can fill
-  const int gx = std::min(a->T, sms * 8);
+  const int gx = std::min((a->T - 1) / A.group + 1, sms * 8);
   const int gy = std::max(1, std::min(need, sms * 2 / gx));
   if (a->src_type == SF_F32)
     launch_append<float>(A, kv.d, dim3(gx, gy), sf::as_cuda(stream));

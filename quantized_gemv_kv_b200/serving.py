@@ -23,6 +23,7 @@ SF_F32, SF_BF16 = 0, 1
 PLAN_OK, PLAN_LENGTH, PLAN_ROWS, PLAN_PAGES = range(4)
 _DTYPES = {torch.float32: SF_F32, torch.bfloat16: SF_BF16}
 _i64 = ctypes.c_int64
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
 class _PagedKV(ctypes.Structure):
@@ -117,19 +118,24 @@ class _Job:
         self._ref = ctypes.byref(args)
         self._keep = keep          # the tensors whose addresses the arguments hold
         self.device = device
+        self._index = device.index
 
     def run(self, stream: torch.cuda.Stream | None = None) -> None:
         """Enqueues the call on ``stream`` (default: the current stream of
         the tensors' device)."""
         if stream is None:
-            stream = torch.cuda.current_stream(self.device)
+            raw = _raw_stream(self._index)  # torch.cuda.current_stream().cuda_stream, without the Stream object
         elif stream.device != self.device:
             raise ValueError(f"stream is on {stream.device}, the tensors on {self.device}")
-        if torch.cuda.current_device() == self.device.index:
-            _check(self._call(self._ref, stream.cuda_stream))
+        else:
+            raw = stream.cuda_stream
+        if _current_device() == self._index:
+            status = self._call(self._ref, raw)
         else:
             with torch.cuda.device(self.device):
-                _check(self._call(self._ref, stream.cuda_stream))
+                status = self._call(self._ref, raw)
+        if status:
+            _check(status)
 
 
 # ---- the pool ------------------------------------------------------------------
