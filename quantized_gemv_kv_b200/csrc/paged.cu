@@ -213,19 +213,22 @@ __global__ void __launch_bounds__(1024) paged_plan_kernel(const __grid_constant_
 // rows' heads.
 //
 // Every result is the fp64 or IEEE one rounded once, as sf_rope and
-// sf_kv_append have it, but computed in fp32 where that cannot differ:
+// sf_kv_append have it, but computed in fp32 where that cannot differ, with one
+// rare branch per token-head for where it might:
 //  * a query is rotated in fp32 and both ends of its error interval rounded to
-//    bf16; only where they differ (one in some thousands) fp64 decides.  The
+//    bf16; where they differ (one entry in some thousands) fp64 decides.  The
 //    conversions to and from fp64 of every query bound the kernel before;
+//  * a scale is (max - min) / 15 rounded to fp32, then fp16: times 1/15, unless
+//    that lies within 4 units of an fp16 midpoint;
 //  * a code is rint(x / s): x times a reciprocal, unless that lies within 2^-16
-//    of a half, where the division decides.
+//    of a half.
 // Bound by memory for many rows (a source value is read once, 4 bits and a bf16
 // come out), so a warp has the sources of the next kAhead rows of a head on
 // their way; by latency for few rows, when a row's heads are spread over
 // blocks.
 
 constexpr int kAppWarps = 8;
-constexpr int kAhead = 4;
+constexpr int kAhead = 2;
 
 struct AppendArgs {
   const void *k, *v, *q;
@@ -289,24 +292,28 @@ __device__ __forceinline__ float warp_min(float v) {
   return m;
 }
 
-// bf16(a c + b s) rounded once; c and s are fp64, ch and sh their fp32 values.
-// In fp32, u = a ch and v = b sh are off by at most 2^-24 |.| each for ch and
-// the product, their sum by 2^-24 of itself: within 2^-22 (|u| + |v|).
-__device__ __forceinline__ uint16_t rotated_bf16(float a, float b, float ch, float sh, const double2* cs, bool second) {
-  const float u = a * ch, r = fmaf(b, sh, u), e = 0x1p-22f * (fabsf(u) + fabsf(b * sh)) + 1e-40f;
-  const uint16_t lo = __bfloat16_as_ushort(__float2bfloat16_rn(r - e));
-  const uint16_t hi = __bfloat16_as_ushort(__float2bfloat16_rn(r + e));
-  if (lo == hi) return lo;
-  const double c = cs->x, s = second ? cs->y : -cs->y;
-  return sfd::to_bf16(static_cast<double>(a) * c + static_cast<double>(b) * s);
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return reinterpret_cast<const uint32_t&>(v);
 }
 
-// clamp(rint(x / s) + z, 0, 15) with the division and rint of IEEE, as a float.
-__device__ __forceinline__ float code_of(float x, float s, float inv, float z) {
-  float r = fminf(fmaxf(x * inv, -32.f), 32.f);  // beyond, the clamp decides
-  float n = (r + 12582912.f) - 12582912.f;       // rint
-  if (fabsf(fabsf(r - n) - 0.5f) < 0x1p-16f) n = rintf(__fdiv_rn(x, s));
-  return fminf(fmaxf(n + z, 0.f), 15.f);
+// (max - min) / 15 as sf_kv_append rounds it; at least the smallest fp16, 1 for 0.
+__device__ __forceinline__ float scale_of(float span) {
+  float q = span * (1.f / 15.f);  // within 2 units of the quotient
+  const uint32_t low = __float_as_uint(q) & 0x1FFFu;
+  if (q < 6.2e-5f || low - 0xFFCu <= 8u) q = __fdiv_rn(span, 15.0f);  // fp16's subnormals, or near a midpoint
+  const float s = __half2float(__float2half_rn(fminf(q, 65504.0f)));
+  return s == 0.f ? 1.f : s;
+}
+
+// rint(x / s) from x times 1/s, clamped to [-32, 32] (beyond, the code's own clamp decides); near: too close to a half.
+__device__ __forceinline__ float quotient(float x, float inv, bool& near) {
+  const float r = fminf(fmaxf(x * inv, -32.f), 32.f), n = (r + 12582912.f) - 12582912.f;
+  near |= fabsf(r - n) > 0.5f - 0x1p-16f;
+  return n;
+}
+__device__ __forceinline__ float exact_quotient(float x, float s) {
+  return fminf(fmaxf(rintf(__fdiv_rn(x, s)), -32.f), 32.f);
 }
 
 template <int D, typename S>
@@ -376,17 +383,41 @@ __global__ void __launch_bounds__(32 * kAppWarps) paged_append_kernel(const __gr
         if (slot < 0 || slot >= A.slot_end) continue;  // the same for the whole warp
         const int64_t t = row0 + row;
         if (kind == 2) {
-          uint16_t ua[NP], ub[NP];
+          // In fp32 with cosine and sine rounded to it: the two products are off by 2^-23 of themselves, the sum by
+          // 2^-24 of itself, together within e.
+          float v[2][NP], e[NP];
+          bool near = false;
+          uint16_t o[2][NP];
 #pragma unroll
           for (int j = 0; j < NP; ++j) {
-            const int i = NP * lane + j;
-            const float2 cs = turn32[buf][row][i];
-            ua[j] = rotated_bf16(lo[k][j], hi[k][j], cs.x, -cs.y, &turn[buf][row][i], false);
-            ub[j] = rotated_bf16(hi[k][j], lo[k][j], cs.x, cs.y, &turn[buf][row][i], true);
+            const float2 cs = turn32[buf][row][NP * lane + j];
+            const float x = lo[k][j], y = hi[k][j], ys = y * cs.y, yc = y * cs.x;
+            v[0][j] = fmaf(x, cs.x, -ys);
+            v[1][j] = fmaf(x, cs.y, yc);
+            e[j] = fmaf(fabsf(x) + fabsf(y), 0x1p-22f, 1e-40f);  // |cosine|, |sine| <= 1
+          }
+#pragma unroll
+          for (int z = 0; z < 2; ++z)
+#pragma unroll
+            for (int j = 0; j < NP; j += 2) {
+              const int i = j + 1 < NP ? j + 1 : j;
+              const uint32_t below = pack_bf16(v[z][j] - e[j], v[z][i] - e[i]);
+              near |= below != pack_bf16(v[z][j] + e[j], v[z][i] + e[i]);
+              o[z][j] = static_cast<uint16_t>(below);
+              if (j + 1 < NP) o[z][i] = static_cast<uint16_t>(below >> 16);
+            }
+          if (near) {
+#pragma unroll
+            for (int j = 0; j < NP; ++j) {
+              const double2 cs = turn[buf][row][NP * lane + j];
+              const double x = lo[k][j], y = hi[k][j];
+              o[0][j] = sfd::to_bf16(x * cs.x - y * cs.y);
+              o[1][j] = sfd::to_bf16(y * cs.x + x * cs.y);
+            }
           }
           uint16_t* out = A.q_out + t * A.q_out_stride + h * D + NP * lane;
-          store_bf16<NP>(out, ua);
-          store_bf16<NP>(out + H, ub);
+          store_bf16<NP>(out, o[0]);
+          store_bf16<NP>(out + H, o[1]);
           continue;
         }
         if (rot && kind == 0) {
@@ -407,15 +438,30 @@ __global__ void __launch_bounds__(32 * kAppWarps) paged_append_kernel(const __gr
         }
         mn = warp_min(mn);
         mx = warp_max(mx);
-        __half s16 = __float2half_rn(fminf(__fdiv_rn(__fsub_rn(mx, mn), 15.0f), 65504.0f));
-        if (__half2float(s16) == 0.0f) s16 = __float2half_rn(1.0f);
-        const float s = __half2float(s16), inv = __frcp_rn(s);
-        const float zf = code_of(-mn, s, inv, 0.f);
+        const float s = scale_of(__fsub_rn(mx, mn));
+        float inv;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+        bool near = false;
+        float zf = quotient(-mn, inv, near), c[2][NP];
+#pragma unroll
+        for (int j = 0; j < NP; ++j) {
+          c[0][j] = quotient(lo[k][j], inv, near);
+          c[1][j] = quotient(hi[k][j], inv, near);
+        }
+        if (near) {
+          zf = exact_quotient(-mn, s);
+#pragma unroll
+          for (int j = 0; j < NP; ++j) {
+            c[0][j] = exact_quotient(lo[k][j], s);
+            c[1][j] = exact_quotient(hi[k][j], s);
+          }
+        }
+        zf = fminf(fmaxf(zf, 0.f), 15.f);
         uint32_t wl = 0, wh = 0;  // the lane's codes at their place in the word
         uint16_t vl[NP], vh[NP];
 #pragma unroll
         for (int j = 0; j < NP; ++j) {
-          const float cl = code_of(lo[k][j], s, inv, zf), ch = code_of(hi[k][j], s, inv, zf);
+          const float cl = fminf(fmaxf(c[0][j] + zf, 0.f), 15.f), ch = fminf(fmaxf(c[1][j] + zf, 0.f), 15.f);
           wl |= (__float_as_uint(cl + 8388608.f) & 15u) << (4 * j);
           wh |= (__float_as_uint(ch + 8388608.f) & 15u) << (4 * j);
           vl[j] = __bfloat16_as_ushort(__float2bfloat16_rn(s * (cl - zf)));
@@ -437,7 +483,7 @@ __global__ void __launch_bounds__(32 * kAppWarps) paged_append_kernel(const __gr
         }
         if (lane == 0)
           (kind ? A.v_param : A.k_param)[r] =
-              static_cast<uint32_t>(__half_as_ushort(s16)) |
+              static_cast<uint32_t>(__half_as_ushort(__float2half_rn(s))) |
               static_cast<uint32_t>(__half_as_ushort(__float2half_rn(zf))) << 16;
         uint16_t* val = kind ? A.v_val : A.k_val;
         if (val != nullptr) {
