@@ -10,6 +10,12 @@ largest scale ks sum |q| 15 of the call a score is within 2^-20 S and a softmax
 weight within 2^-19 S relatively.  Weights enter the value product with 2^-22,
 and a chain of L/16 products with 16 terms each is summed in fp32, so with V
 the largest |v|: |out - exact| <= 2 V (2^-19 S + 2^-21 + (64 + L/16) 2^-24).
+For bf16 outputs q enters in 15-bit fixed point: an entry is off by up to
+2^-15 qmax (uniform, sigma 2^-15.8 qmax), so a score by a sum of d such errors
+times scale ks |c - z| (rms at most 8): six sigma of that is E = 6 2^-15.8 qmax
+8 sqrt(d) scale ks, a weight is off by 2 E + 2^-11 relatively, and 2 V (2 E +
+2^-11) is added; over all outputs the errors are independent, so their 2-norm
+is within 2^-8 of the outputs'.
 Adapters: fp32 sums of at most K + rank + 40 terms, in chains of 16, so
 |out - exact| <= 2^-24 (|out| + (K/8 + rank/8 + 40) M), M = scale |B| (|A| |x|).
 """
@@ -329,9 +335,12 @@ class _Case:
         S = scale * ks * np.abs(q).sum(-1).max() * 15
         V = np.abs(self.val[1]).max()
         tol = 2 * V * (2.0 ** -19 * S + 2.0 ** -21 + (64 + max(self.lens) / 16) * 2.0 ** -24)
-        if out_type == torch.bfloat16:
-            tol = tol + BF16 * np.abs(want)
         err = np.abs(out - want)
+        if out_type == torch.bfloat16:
+            E = 6 * 2.0 ** -15.8 * np.abs(q).max() * 8 * np.sqrt(q.shape[-1]) * scale * ks
+            tol = tol + BF16 * np.abs(want) + 2 * V * (2 * E + 2.0 ** -11)
+            rows = slice(0, self.cu[-1])
+            assert np.linalg.norm(err[rows]) <= 2.0 ** -8 * np.linalg.norm(want[rows])
         assert np.all(err <= tol), (err.max(), np.max(tol))
         assert np.all(out[self.cu[-1]:] == 7.0)
         return err.max()
@@ -340,8 +349,9 @@ class _Case:
 @pytest.mark.parametrize("Hq,Hkv,d,P", [(32, 8, 128, 64), (1, 1, 128, 16), (8, 8, 64, 16), (8, 1, 128, 32),
                                         (10, 2, 128, 128), (16, 1, 64, 256), (4, 2, 256, 16), (8, 1, 256, 64),
                                         (33, 3, 128, 16), (64, 1, 128, 16)])
-def test_attention_head_layouts(sf, Hq, Hkv, d, P):
-    _Case(sf, Hq + d, [1, 1, 1], [37, 300, 129], Hq, Hkv, d, P).check(sf)
+@pytest.mark.parametrize("out_type", [torch.float32, torch.bfloat16])
+def test_attention_head_layouts(sf, Hq, Hkv, d, P, out_type):
+    _Case(sf, Hq + d, [1, 1, 1], [37, 300, 129], Hq, Hkv, d, P).check(sf, out_type)
 
 
 @pytest.mark.parametrize("P", [16, 64])
@@ -355,10 +365,12 @@ def test_attention_lengths(sf, d, P):
 
 
 @pytest.mark.parametrize("Hq,Hkv,d", [(8, 2, 128), (8, 8, 64), (5, 1, 128), (4, 1, 256)])
-@pytest.mark.parametrize("window", [0, 1, 16, 70])
-def test_attention_rows_and_windows(sf, Hq, Hkv, d, window):
+@pytest.mark.parametrize("window,out_type", [(0, torch.float32), (1, torch.float32), (16, torch.float32),
+                                             (70, torch.float32), (0, torch.bfloat16), (70, torch.bfloat16)])
+def test_attention_rows_and_windows(sf, Hq, Hkv, d, window, out_type):
     """Several rows per request (causal), more rows than tokens (the first rows see none), sliding windows."""
-    _Case(sf, 5 + window, [4, 1, 7, 20, 3, 33], [200, 70, 7, 65, 1, 300], Hq, Hkv, d, 16).check(sf, window=window)
+    _Case(sf, 5 + window, [4, 1, 7, 20, 3, 33], [200, 70, 7, 65, 1, 300], Hq, Hkv, d, 16).check(
+        sf, out_type, window=window)
 
 
 @pytest.mark.parametrize("out_type", [torch.float32, torch.bfloat16])
