@@ -883,8 +883,8 @@ sf_status sf_paged_append(const sf_paged_append_args* a, sf_stream_t stream);
  * as f16 pairs (22 bits); all sums are fp32.  The order of sums is fixed by
  * the arguments' values, so equal calls give equal bits.
  * Constraints: kv's; Hq a multiple of Hkv, Hq/Hkv <= 64, 1 <= R <= 8192,
- *   T >= 0, max_pages >= 1, max_pages * page_size < 2^31, window >= 0, scale
- *   finite; rows of q and out 16-byte aligned.
+ *   T >= 0, T * Hq/Hkv < 2^26, max_pages >= 1, max_pages * page_size < 2^31,
+ *   window >= 0, scale finite; rows of q and out 16-byte aligned.
  */
 typedef struct sf_attn_paged_args {
   const sf_paged_kv* kv;

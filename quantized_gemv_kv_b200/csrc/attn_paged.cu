@@ -15,6 +15,7 @@ struct AttnArgs {
   int64_t q_stride, out_stride, table_stride, page_rows;
   float scale;
   int T, R, Hq, Hkv, group, shift, num_pages, max_pages, window, bf16_out;
+  uint32_t per_group;  // ceil(2^32 / group): columns are below 2^26, so its high product is the quotient; 0 for 1
 };
 
 // How the work is laid out.  A request's rows times the query heads of one KV
@@ -47,7 +48,7 @@ struct AttnArgs {
 //    largest seen); movmatrix turns them from score order to operand order.  The
 //    tensor cores truncate their fp32 sums, so a chain of them drifts (7e-6 over
 //    a run of 112): after kFlush stages the sums are added, rounded, to sums in
-//    the workspace and start again;
+//    shared memory and start again (kept in the workspace, those cost 20%);
 //  * PACK, up to 4 columns (a decode step with 4 query heads per KV head): the
 //    score products' 16 columns are digit 0, digit 1 and twice digit 2 of the
 //    four, so a lane keeps one of its two tokens and half the softmax work, and
@@ -87,7 +88,7 @@ struct Cfg {
   static constexpr int PART = COLS * (D + 1);  // floats of one partial: the columns' outputs, then their log sums
   static constexpr int SUMS = MT * NT * 4 * 32;  // a warp's value sums
   static constexpr int RINGB = STAGES * STAGEB;
-  static constexpr int SMEM = WARPS * RINGB;
+  static constexpr int SMEM = WARPS * (RINGB + SUMS * 4);  // the rings, then each warp's flushed sums
   static_assert(!PACK || NT == 1, "packed columns are one tile");
   static_assert(PART * 4 <= RINGB, "a warp's partial takes its ring's place");
   static_assert(SMEM <= 224 * 1024, "shared memory");
@@ -190,6 +191,11 @@ __device__ __forceinline__ uint32_t h2_bits(float a, float b) {
   return reinterpret_cast<const uint32_t&>(h);
 }
 
+// Column c's row: c / group.
+__device__ __forceinline__ int row_of(const AttnArgs& A, int c) {
+  return A.per_group == 0 ? c : static_cast<int>(__umulhi(static_cast<uint32_t>(c), A.per_group));
+}
+
 // One request's columns and stages.
 struct Req {
   int row0, rows;    // its rows in q and out (those below T)
@@ -248,7 +254,6 @@ struct Work {
   AttnArgs a;
   Tail* tails;    // [blocks]
   float* parts;   // [blocks][2][PART]: a block's part of a segment begun earlier (0), of its open one (1)
-  float* flushed; // [blocks][WARPS][SUMS]: a warp's flushed sums
   float* heads;   // [blocks][WARPS][PART]: a warp's part of a segment begun before its run, when the run goes on
   int blocks;
 };
@@ -276,8 +281,8 @@ template <class C>
 __device__ __forceinline__ void put(const AttnArgs& A, const Req& q, int block, int h, int col, int x, float4 v) {
   const int c = block * C::COLS + col;
   if (c >= q.rows * A.group) return;
-  const int64_t at = (q.row0 + c / A.group) * A.out_stride +
-                     static_cast<int64_t>(h * A.group + c % A.group) * C::D + x;
+  const int r = row_of(A, c);
+  const int64_t at = (q.row0 + r) * A.out_stride + static_cast<int64_t>(h * A.group + c - r * A.group) * C::D + x;
   if (A.bf16_out) {
     __nv_bfloat162 b[2] = {__floats2bfloat162_rn(v.x, v.y), __floats2bfloat162_rn(v.z, v.w)};
     *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(A.out) + at) = *reinterpret_cast<const uint2*>(b);
@@ -339,6 +344,8 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) attn_paged_kernel(const __gr
   const AttnArgs& A = W.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const int group = A.group;
+
+  asm volatile("griddepcontrol.launch_dependents;");  // the join waits for this grid's end
 
   // The units of all requests.
   const int per = (A.R + NTHR - 1) / NTHR;
@@ -474,9 +481,9 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) attn_paged_kernel(const __gr
     int all_hi = 0, all_lo = 0;  // tokens in [all_lo, all_hi) are seen by every column
     int any_hi = 0, any_lo = 0;  // those outside [any_lo, any_hi) by none
     float acc[MT][NT][4];  // the value sums since the last flush
-    float* const flushed = W.flushed + (static_cast<int64_t>(blockIdx.x) * C::WARPS + warp) * C::SUMS + lane;
+    float* const flushed = reinterpret_cast<float*>(smem + C::WARPS * C::RINGB) + warp * C::SUMS + lane;
     int since = 0;         // stages in acc
-    bool has_flushed = false;
+    bool has_flushed = false, empty = true;  // empty: nothing in acc yet
     float vscale = 0.f;  // power of two that the value scales are multiplied by
     int slot = 0;
     bool fresh = true;
@@ -498,24 +505,27 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) attn_paged_kernel(const __gr
     for (int u = 0; u < count; ++u) {
       if (fresh) {
         fresh = false;
+        empty = true;
         vscale = 0.f;
         const int h = cons.h, c0 = cons.block * C::COLS, cols = cons.q.rows * group;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           const int c = c0 + (PACK ? g & 3 : 8 * n + g);
           uint4 w[KW];
-          const uint16_t* src = A.q + (cons.q.row0 + c / group) * A.q_stride +
-                                static_cast<int64_t>(h * group + c % group) * D + 8 * KW * t;
-          uint32_t big = 0;
+          const int r = row_of(A, c);
+          const uint16_t* src = A.q + (cons.q.row0 + r) * A.q_stride +
+                                static_cast<int64_t>(h * group + c - r * group) * D + 8 * KW * t;
+          uint32_t big = 0;  // two halves
 #pragma unroll
           for (int j = 0; j < KW; ++j) {
             w[j] = c < cols ? *reinterpret_cast<const uint4*>(src + 8 * j) : make_uint4(0, 0, 0, 0);
             const uint32_t* p = reinterpret_cast<const uint32_t*>(&w[j]);
 #pragma unroll
-            for (int z = 0; z < 4; ++z) big = max(big, max(p[z] & 0x7FFFu, (p[z] >> 16) & 0x7FFFu));
+            for (int z = 0; z < 4; ++z) big = __vmaxu2(big, p[z] & 0x7FFF7FFFu);
           }
-          big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
-          big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+          big = __vmaxu2(big, __shfl_xor_sync(0xffffffffu, big, 1));
+          big = __vmaxu2(big, __shfl_xor_sync(0xffffffffu, big, 2));
+          big = max(big >> 16, big & 0xFFFFu);
           const bool finite = big < 0x7F80u;
           const int e = finite ? max(static_cast<int>(big >> 7) - 127, -100) : 0;
           constexpr int kExp = C::BF16 ? 14 : 21;
@@ -531,7 +541,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) attn_paged_kernel(const __gr
 #pragma unroll
             for (int z = 0; z < 8; ++z) {  // dim 8 (KW t + j) + z
               const float v = __uint_as_float((z & 1) ? p[z >> 1] & 0xFFFF0000u : p[z >> 1] << 16);
-              const uint32_t X = __float_as_uint(fmaf(finite ? v : 0.f, up, 12582912.f)) - 0x4B400000u;
+              const uint32_t X = __float_as_uint(fmaf(v, up, 12582912.f)) - 0x4B400000u;  // (any, if not finite)
               sum += static_cast<int>(X);
               constexpr uint32_t kBias = C::BF16 ? 0x8080u : 0x808080u;
               y[z] = (X + kBias) ^ kBias;
@@ -566,14 +576,15 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) attn_paged_kernel(const __gr
             qsum[n][z] = (C::SPLIT ? 16.f : 1.f) * static_cast<float>(__shfl_sync(0xffffffffu, sum, from));
             qsc[n][z] = __shfl_sync(0xffffffffu, sc, from);
             const int cc = c0 + 8 * n + col0 + z;
-            const int p = cons.q.len - (cons.q.last - (cons.q.row0 + cc / group));
+            const int p = cons.q.len - (cons.q.last - (cons.q.row0 + row_of(A, cc)));
             lim_hi[n][z] = cc < cols ? p + 1 : INT_MAX;
             lim_lo[n][z] = cc < cols && A.window > 0 ? p + 1 - A.window : INT_MIN;
             m[n][z] = -INFINITY;
             l[n][z] = zs[n][z] = 0.f;
           }
         }
-        const int r_first = cons.q.row0 + c0 / group, r_last = cons.q.row0 + (min(c0 + C::COLS, cols) - 1) / group;
+        const int r_first = cons.q.row0 + row_of(A, c0);
+        const int r_last = cons.q.row0 + row_of(A, min(c0 + C::COLS, cols) - 1);
         all_hi = cons.q.len - (cons.q.last - r_first) + 1;
         any_hi = cons.q.len - (cons.q.last - r_last) + 1;
         all_lo = A.window > 0 ? any_hi - A.window : 0;
@@ -603,7 +614,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) attn_paged_kernel(const __gr
       const uint32_t* vpar = kpar + TOK;
       const int tok0 = (cons.q.st0 + cons.tile) * TOK + sub * C::SUB;
       // a token of the step does not exist, or not every column sees every token
-      const bool odd = __any_sync(0xffffffffu, (kpar[lane] & 0xFFFFu) == 0) || tok0 + C::SUB > all_hi || tok0 < all_lo;
+      const bool odd = __any_sync(0xffffffffu, (kpar[lane % C::SUB] & 0xFFFFu) == 0) || tok0 + C::SUB > all_hi || tok0 < all_lo;
 
       // scores in base 2: tokens tok_of[k] x columns col0, col0 + 1
       float s[TILES][NT][ROWS][2];
@@ -738,6 +749,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) attn_paged_kernel(const __gr
             alpha[n][z] *= grow;
             zs[n][z] *= alpha[n][z];
           }
+        if (!empty) {
         // the value product's columns 2t, 2t + 1 belong to the lane's score columns (packed: as weights or remainders)
 #pragma unroll
         for (int k = 0; k < MT; ++k)
@@ -755,7 +767,9 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) attn_paged_kernel(const __gr
 #pragma unroll
               for (int z = 0; z < 4; ++z) flushed[((k * NT + n) * 4 + z) * 32] *= alpha[n][z & 1];
         }
+        }
       }
+      empty = false;
 
       // weights as operand fragments
       constexpr int WT = PACK || C::BF16 ? 1 : 2;  // products of 8 columns per column tile
@@ -968,6 +982,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) attn_paged_kernel(const __gr
 template <class C>
 __global__ void __launch_bounds__(32 * C::COLS) attn_paged_join_kernel(const __grid_constant__ Work W) {
   constexpr int D = C::D;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const Tail tail = W.tails[blockIdx.x];
   if (!tail.open) return;
   const int b = blockIdx.x, n = tail.last_cta - b + 1, col = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1000,7 +1015,7 @@ size_t tails_bytes(int blocks) { return (blocks * sizeof(Tail) + 255) / 256 * 25
 template <class C>
 struct Kernel {
   static size_t bytes(int blocks) {
-    return tails_bytes(blocks) + static_cast<size_t>(blocks) * ((2 + C::WARPS) * C::PART + C::WARPS * C::SUMS) * sizeof(float);
+    return tails_bytes(blocks) + static_cast<size_t>(blocks) * (2 + C::WARPS) * C::PART * sizeof(float);
   }
   static sf_status launch(const AttnArgs& A, void* ws, int blocks, cudaStream_t s) {
     Work W{};
@@ -1008,13 +1023,22 @@ struct Kernel {
     W.tails = static_cast<Tail*>(ws);
     W.parts = reinterpret_cast<float*>(static_cast<char*>(ws) + tails_bytes(blocks));
     W.heads = W.parts + static_cast<size_t>(blocks) * 2 * C::PART;
-    W.flushed = W.heads + static_cast<size_t>(blocks) * C::WARPS * C::PART;
     W.blocks = blocks;
     SF_CHECK_CUDA(cudaFuncSetAttribute(attn_paged_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
     attn_paged_kernel<C><<<blocks, 32 * C::WARPS, C::SMEM, s>>>(W);
     sf_status st = sf::check_launch("attn_paged_kernel");
     if (st != SF_OK) return st;
-    attn_paged_join_kernel<C><<<blocks, 32 * C::COLS, 0, s>>>(W);
+    // launched while the first kernel runs; its blocks start as that one's end, and wait for the last
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(32 * C::COLS);
+    cfg.stream = s;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    SF_CHECK_CUDA(cudaLaunchKernelEx(&cfg, attn_paged_join_kernel<C>, W));
     return sf::check_launch("attn_paged_join_kernel");
   }
 };
@@ -1031,12 +1055,12 @@ auto with_kernel(int T, int R, int Hq, int Hkv, int d, F f) {
     return f(Kernel<Cfg<64, 2, false, BF16, 64, 8, 3>>{});
   }
   if (d == 128) {
-    if (cols <= 4) return f(Kernel<Cfg<128, 1, true, BF16, 64, 12, 2>>{});
+    if (cols <= 4) return f(Kernel<Cfg<128, 1, true, BF16, 64, 8, 2>>{});
     if (cols <= 8) return f(Kernel<Cfg<128, 1, false, BF16, 64, 8, 2>>{});
     return f(Kernel<Cfg<128, 2, false, BF16, 64, 8, 2>>{});
   }
-  if (cols <= 4) return f(Kernel<Cfg<256, 1, true, BF16, 32, 8, 3>>{});
-  return f(Kernel<Cfg<256, 1, false, BF16, 32, 8, 3>>{});
+  if (cols <= 4) return f(Kernel<Cfg<256, 1, true, BF16, 32, 8, 2>>{});
+  return f(Kernel<Cfg<256, 1, false, BF16, 32, 8, 2>>{});
 }
 
 }  // namespace
@@ -1066,6 +1090,7 @@ extern "C" sf_status sf_attn_paged(const sf_attn_paged_args* a, sf_stream_t stre
   SF_REQUIRE(a->max_pages >= 1 && static_cast<int64_t>(a->max_pages) * kv.page_size < (1ll << 31),
              "%s: need max_pages >= 1 and max_pages * page_size < 2^31", what);
   SF_REQUIRE(a->table_stride >= a->max_pages, "%s: table_stride is below max_pages", what);
+  SF_REQUIRE(static_cast<int64_t>(a->T) * (a->Hq / kv.Hkv) < (1 << 26), "%s: T * Hq/Hkv must be below 2^26", what);
   SF_REQUIRE(a->window >= 0, "%s: window must be >= 0", what);
   SF_REQUIRE(std::isfinite(a->scale), "%s: scale must be finite", what);
   SF_REQUIRE(a->out_type == SF_F32 || a->out_type == SF_BF16, "%s: out_type must be SF_F32 or SF_BF16", what);
@@ -1098,6 +1123,7 @@ extern "C" sf_status sf_attn_paged(const sf_attn_paged_args* a, sf_stream_t stre
   A.Hq = a->Hq;
   A.Hkv = kv.Hkv;
   A.group = a->Hq / kv.Hkv;
+  A.per_group = A.group == 1 ? 0 : static_cast<uint32_t>(((1ull << 32) + A.group - 1) / A.group);
   A.shift = sf::log2i(kv.page_size);
   A.num_pages = kv.num_pages;
   A.max_pages = a->max_pages;
