@@ -1,5 +1,6 @@
 // sf_attn_paged: attention of a step's rows over a paged 4-bit KV cache.
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cmath>
 
@@ -25,7 +26,8 @@ struct AttnArgs {
 // and every block (and in it every warp) takes an equal run of them, so a
 // 128K-token request and a hundred short ones fill the SMs alike.  A segment
 // that lies within one warp's run is written by it; the parts of one that does
-// not are joined in shared memory, and across blocks by a second kernel.
+// not are joined in shared memory, and across blocks by a second kernel (the last
+// block to arrive doing it instead was slower: two fences, and the same reads).
 //
 // A warp's stage of 16-token tiles:
 //  * scores: mma.m16n8k32 (s8), rows = tokens, columns = query columns.  A
@@ -77,7 +79,9 @@ struct Cfg {
   static constexpr bool PACK = PACK_, BF16 = BF16_;
   static constexpr int DIGITS = BF16 ? 2 : 3;
   static constexpr int COLS = PACK ? 4 : 8 * NT, GROUPS = TOK / 16;
-  static constexpr int TILES = 2, SUB = 16 * TILES;            // tiles and tokens of a step of the inner loop
+  // tiles and tokens of a step of the inner loop: four tiles where the registers allow (128K tokens: 42 us; two, 45)
+  static constexpr int TILES = NT == 1 && D <= 128 && WARPS == 8 ? 4 : 2, SUB = 16 * TILES;
+  static_assert(TOK % SUB == 0, "whole steps");
   static constexpr bool SPLIT = NT == 1;  // odd codes as 16 c in sums of their own: fewer shifts, more sums
   static constexpr int DT = PACK ? DIGITS - 1 : DIGITS;                      // products of 8 columns per k step and column tile
   static constexpr int ROWS = PACK ? 1 : 2;                    // tokens of a tile whose scores a lane keeps
@@ -86,6 +90,7 @@ struct Cfg {
   static constexpr int PAR = 2 * TOK * ROWB;                          // offset of the params in a stage
   static constexpr int STAGEB = PAR + 2 * TOK * 4;
   static constexpr int PART = COLS * (D + 1);  // floats of one partial: the columns' outputs, then their log sums
+  static constexpr int JOIN = COLS == 4 ? 4 : 2;  // warps a column of the second kernel
   static constexpr int SUMS = MT * NT * 4 * 32;  // a warp's value sums
   static constexpr int RINGB = STAGES * STAGEB;
   static constexpr int SMEM = WARPS * (RINGB + SUMS * 4);  // the rings, then each warp's flushed sums
@@ -245,9 +250,10 @@ __device__ __forceinline__ void advance(const AttnArgs& A, Cursor& c) {
 // What the second kernel needs of a block: the segment that starts in it and
 // ends in a later block.
 struct Tail {
-  int open;        // 1: there is one
-  int i, block, h; // which
-  int last_cta;    // the block that holds its last unit
+  int open;         // 1: there is one
+  int row0, rows;   // its request's
+  int block, h;     // which of the request's
+  int last_cta;     // the block that holds its last unit
 };
 
 struct Work {
@@ -278,11 +284,11 @@ struct Runs {
 
 // Dims x .. x + 3 of a column of a segment.
 template <class C>
-__device__ __forceinline__ void put(const AttnArgs& A, const Req& q, int block, int h, int col, int x, float4 v) {
+__device__ __forceinline__ void put(const AttnArgs& A, int row0, int rows, int block, int h, int col, int x, float4 v) {
   const int c = block * C::COLS + col;
-  if (c >= q.rows * A.group) return;
+  if (c >= rows * A.group) return;
   const int r = row_of(A, c);
-  const int64_t at = (q.row0 + r) * A.out_stride + static_cast<int64_t>(h * A.group + c - r * A.group) * C::D + x;
+  const int64_t at = (row0 + r) * A.out_stride + static_cast<int64_t>(h * A.group + c - r * A.group) * C::D + x;
   if (A.bf16_out) {
     __nv_bfloat162 b[2] = {__floats2bfloat162_rn(v.x, v.y), __floats2bfloat162_rn(v.z, v.w)};
     *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(A.out) + at) = *reinterpret_cast<const uint2*>(b);
@@ -338,7 +344,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) attn_paged_kernel(const __gr
   struct Part {
     long long us, ue;  // the segment's units; us < 0: none
     const float* at;
-    int i, block, h;
+    int row0, rows, block, h;
   };
   __shared__ Part parts[C::WARPS][2];  // of the segment begun before the warp's run, and of the one that goes on behind
   const AttnArgs& A = W.a;
@@ -614,7 +620,10 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) attn_paged_kernel(const __gr
       const uint32_t* vpar = kpar + TOK;
       const int tok0 = (cons.q.st0 + cons.tile) * TOK + sub * C::SUB;
       // a token of the step does not exist, or not every column sees every token
-      const bool odd = __any_sync(0xffffffffu, (kpar[lane % C::SUB] & 0xFFFFu) == 0) || tok0 + C::SUB > all_hi || tok0 < all_lo;
+      bool odd = false;
+#pragma unroll
+      for (int z = 0; z < C::SUB; z += 32) odd |= (kpar[z + lane] & 0xFFFFu) == 0;
+      odd = __any_sync(0xffffffffu, odd) || tok0 + C::SUB > all_hi || tok0 < all_lo;
 
       // scores in base 2: tokens tok_of[k] x columns col0, col0 + 1
       float s[TILES][NT][ROWS][2];
@@ -896,7 +905,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) attn_paged_kernel(const __gr
               for (int z = 0; z < 2; ++z)
 #pragma unroll
                 for (int k = 0; k < MT; k += 2)
-                  put<C>(A, cons.q, cons.block, cons.h, 8 * n + col0 + z, D / 8 * g + 2 * k,
+                  put<C>(A, cons.q.row0, cons.q.rows, cons.block, cons.h, 8 * n + col0 + z, D / 8 * g + 2 * k,
                          make_float4(acc[k][n][z], acc[k][n][z + 2], acc[k + 1][n][z], acc[k + 1][n][z + 2]));
           }
         } else {
@@ -918,7 +927,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) attn_paged_kernel(const __gr
                 if (g == 0) keep[C::COLS * D + col] = l[n][z] == 0.f ? -INFINITY : m[n][z] + log2f(l[n][z]);
               }
           }
-          if (lane == 0) parts[warp][which] = Part{lo + seg_at, lo + seg_end, keep, cons.i, cons.block, cons.h};
+          if (lane == 0) parts[warp][which] = Part{lo + seg_at, lo + seg_end, keep, cons.q.row0, cons.q.rows, cons.block, cons.h};
         }
         fresh = true;
         seg_at = u + 1;
@@ -928,65 +937,70 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) attn_paged_kernel(const __gr
   }
 
   // Segments that are split over the block's warps: the one begun in an earlier block, if any, then those begun in
-  // each warp's run.  A warp per column; lane k looks at part k.
+  // each warp's run.  A warp per segment and column; lane k looks at part k.
   __syncthreads();
   static_assert(2 * C::WARPS <= 32, "a lane per part");
-  const Part mine_p = lane < 2 * C::WARPS ? parts[lane >> 1][lane & 1] : Part{-1, 0, nullptr, 0, 0, 0};
-  bool open = false;
-  unsigned starts = __ballot_sync(0xffffffffu, mine_p.us >= 0 && (lane & 1));
+  const Part mine_p = lane < 2 * C::WARPS ? parts[lane >> 1][lane & 1] : Part{-1, 0, nullptr, 0, 0, 0, 0};
+  const unsigned starts = __ballot_sync(0xffffffffu, mine_p.us >= b_lo && (lane & 1));
   const unsigned early_parts = __ballot_sync(0xffffffffu, mine_p.us >= 0 && mine_p.us < b_lo);
-  for (bool first = early_parts != 0; first || starts != 0;) {
-    const int from = first ? __ffs(early_parts) - 1 : __ffs(starts) - 1;
-    if (!first) starts &= starts - 1;
-    first = false;
+  if (warp == C::WARPS - 1) {
+    const bool open = mine_p.us >= b_lo && mine_p.ue > b_hi && (lane & 1);
+    if (open)
+      W.tails[blockIdx.x] = Tail{1, mine_p.row0, mine_p.rows, mine_p.block, mine_p.h, runs.of(mine_p.ue - 1)};
+    if (!__any_sync(0xffffffffu, open) && lane == 0) W.tails[blockIdx.x].open = 0;
+  }
+  const int chains = __popc(starts) + (early_parts != 0);
+  for (int task = warp; task < chains * C::COLS; task += C::WARPS) {
+    const int col = task % C::COLS;
+    int nth = task / C::COLS;
+    unsigned rest = starts;
+    int from = __ffs(early_parts) - 1;
+    if (early_parts == 0 || nth-- > 0) {
+      for (int k = 0; k < nth; ++k) rest &= rest - 1;
+      from = __ffs(rest) - 1;
+    }
     const Part& p = parts[from >> 1][from & 1];
     const bool early = p.us < b_lo, late = p.ue > b_hi;
     const unsigned members = __ballot_sync(0xffffffffu, mine_p.us == p.us);
     // lane k: the k-th member
     const int n = __popc(members);
-    unsigned rest = members;
+    rest = members;
     for (int k = 0; k < min(lane, n - 1); ++k) rest &= rest - 1;
     const int k_th = __ffs(rest) - 1;
     const float* at = parts[k_th >> 1][k_th & 1].at;
-    for (int col = warp; col < C::COLS; col += C::WARPS) {
-      const float lse = lane < n ? at[C::COLS * D + col] : -INFINITY;
-      const float top = warp_top(lse);
-      float sum = 0.f;
-      float4 o[(D + 127) / 128] = {};
-      join_column<C>(at, n, col, lse, top, sum, o);
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const float lse = lane < n ? at[C::COLS * D + col] : -INFINITY;
+    const float top = warp_top(lse);
+    float sum = 0.f;
+    float4 o[(D + 127) / 128] = {};
+    join_column<C>(at, n, col, lse, top, sum, o);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    float* to = W.parts + (static_cast<int64_t>(blockIdx.x) * 2 + (early ? 0 : 1)) * C::PART;
 #pragma unroll
-      for (int z = 0; z < (D + 127) / 128; ++z) {
-        const int dim = 4 * lane + 128 * z;
-        if (dim >= D) continue;
-        const float4 v = make_float4(o[z].x * inv, o[z].y * inv, o[z].z * inv, o[z].w * inv);
-        if (!early && !late)
-          put<C>(A, load_req<C>(A, p.i), p.block, p.h, col, dim, v);
-        else
-          *reinterpret_cast<float4*>(W.parts + (static_cast<int64_t>(blockIdx.x) * 2 + (early ? 0 : 1)) * C::PART +
-                                     col * D + dim) = v;
-      }
-      if ((early || late) && lane == 0)
-        W.parts[(static_cast<int64_t>(blockIdx.x) * 2 + (early ? 0 : 1)) * C::PART + C::COLS * D + col] =
-            sum == 0.f ? -INFINITY : top + log2f(sum);
+    for (int z = 0; z < (D + 127) / 128; ++z) {
+      const int dim = 4 * lane + 128 * z;
+      if (dim >= D) continue;
+      const float4 v = make_float4(o[z].x * inv, o[z].y * inv, o[z].z * inv, o[z].w * inv);
+      if (!early && !late)
+        put<C>(A, p.row0, p.rows, p.block, p.h, col, dim, v);
+      else
+        *reinterpret_cast<float4*>(to + col * D + dim) = v;
     }
-    if (!early && late) {
-      open = true;
-      if (tid == 0) W.tails[blockIdx.x] = Tail{1, p.i, p.block, p.h, runs.of(p.ue - 1)};
-    }
+    if ((early || late) && lane == 0) to[C::COLS * D + col] = sum == 0.f ? -INFINITY : top + log2f(sum);
   }
-  if (!open && tid == 0) W.tails[blockIdx.x].open = 0;
 }
 
-// Joins the parts of the segment that starts in block b and ends in a later one: a warp per column.
+// Joins the parts of the segment that starts in block b and ends in a later one: SPLIT warps per column, each taking
+// every SPLIT-th part, so that all their loads are on their way at once.
 template <class C>
-__global__ void __launch_bounds__(32 * C::COLS) attn_paged_join_kernel(const __grid_constant__ Work W) {
-  constexpr int D = C::D;
+__global__ void __launch_bounds__(32 * C::COLS * C::JOIN) attn_paged_join_kernel(const __grid_constant__ Work W) {
+  constexpr int D = C::D, Z = (D + 127) / 128;
+  __shared__ float sum_sh[C::JOIN][C::COLS];
+  __shared__ float4 o_sh[C::JOIN][C::COLS][Z][32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Tail tail = W.tails[blockIdx.x];
   if (!tail.open) return;
-  const int b = blockIdx.x, n = tail.last_cta - b + 1, col = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Req q = load_req<C>(W.a, tail.i);
+  const int b = blockIdx.x, n = tail.last_cta - b + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int col = warp % C::COLS, share = warp / C::COLS;
   auto part = [&](int k) { return W.parts + (static_cast<int64_t>(b + k) * 2 + (k == 0 ? 1 : 0)) * C::PART; };
   float top = -INFINITY;
   for (int k = lane; k < n; k += 32) {
@@ -995,17 +1009,35 @@ __global__ void __launch_bounds__(32 * C::COLS) attn_paged_join_kernel(const __g
   }
   top = warp_top(top);
   float sum = 0.f;
-  float4 o[(D + 127) / 128] = {};
-  for (int k0 = 0; k0 < n; k0 += 32) {
-    const int k = min(k0 + lane, n - 1);
-    const float lse = k0 + lane < n ? part(k)[C::COLS * D + col] : -INFINITY;
-    join_column<C>(part(k), min(32, n - k0), col, lse, top, sum, o);
+  float4 o[Z] = {};
+  const int mine = n > share ? (n - 1 - share) / C::JOIN + 1 : 0;  // parts share, share + JOIN, ...
+  for (int k0 = 0; k0 < mine; k0 += 32) {
+    const int k = share + C::JOIN * min(k0 + lane, mine - 1);
+    const float lse = k0 + lane < mine ? part(k)[C::COLS * D + col] : -INFINITY;
+    join_column<C>(part(k), min(32, mine - k0), col, lse, top, sum, o);
+  }
+#pragma unroll
+  for (int z = 0; z < Z; ++z) o_sh[share][col][z][lane] = o[z];
+  if (lane == 0) sum_sh[share][col] = sum;
+  __syncthreads();
+  if (share != 0) return;
+#pragma unroll
+  for (int v = 1; v < C::JOIN; ++v) {
+    sum += sum_sh[v][col];
+#pragma unroll
+    for (int z = 0; z < Z; ++z) {
+      const float4 x = o_sh[v][col][z][lane];
+      o[z].x += x.x;
+      o[z].y += x.y;
+      o[z].z += x.z;
+      o[z].w += x.w;
+    }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
-  for (int z = 0; z < (D + 127) / 128; ++z)
+  for (int z = 0; z < Z; ++z)
     if (4 * lane + 128 * z < D)
-      put<C>(W.a, q, tail.block, tail.h, col, 4 * lane + 128 * z,
+      put<C>(W.a, tail.row0, tail.rows, tail.block, tail.h, col, 4 * lane + 128 * z,
              make_float4(o[z].x * inv, o[z].y * inv, o[z].z * inv, o[z].w * inv));
 }
 
@@ -1024,14 +1056,21 @@ struct Kernel {
     W.parts = reinterpret_cast<float*>(static_cast<char*>(ws) + tails_bytes(blocks));
     W.heads = W.parts + static_cast<size_t>(blocks) * 2 * C::PART;
     W.blocks = blocks;
-    SF_CHECK_CUDA(cudaFuncSetAttribute(attn_paged_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
+    static std::atomic<unsigned long long> allowed{0};  // devices that have been told of the kernel's shared memory
+    int dev = 0;
+    SF_CHECK_CUDA(cudaGetDevice(&dev));
+    const unsigned long long bit = 1ull << (dev & 63);
+    if ((allowed.load(std::memory_order_relaxed) & bit) == 0) {
+      SF_CHECK_CUDA(cudaFuncSetAttribute(attn_paged_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
+      if (dev < 64) allowed.fetch_or(bit, std::memory_order_relaxed);
+    }
     attn_paged_kernel<C><<<blocks, 32 * C::WARPS, C::SMEM, s>>>(W);
     sf_status st = sf::check_launch("attn_paged_kernel");
     if (st != SF_OK) return st;
     // launched while the first kernel runs; its blocks start as that one's end, and wait for the last
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(blocks);
-    cfg.blockDim = dim3(32 * C::COLS);
+    cfg.blockDim = dim3(32 * C::COLS * C::JOIN);
     cfg.stream = s;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
