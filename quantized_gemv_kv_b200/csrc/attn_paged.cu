@@ -49,8 +49,9 @@ struct AttnArgs {
 //    its f16 remainder (22 bits; v_s scaled by a power of two that follows the
 //    largest seen); movmatrix turns them from score order to operand order.  The
 //    tensor cores truncate their fp32 sums, so a chain of them drifts (7e-6 over
-//    a run of 112): after kFlush stages the sums are added, rounded, to sums in
-//    shared memory and start again (kept in the workspace, those cost 20%);
+//    a run of 112): after FLUSH stages the sums are added, rounded, to sums in
+//    shared memory and start again (128K tokens: 1.4e-6 off with four stages for
+//    45.8 us, 4.4e-6 with none for 45.0; sums in the workspace cost 20%);
 //  * PACK, up to 4 columns (a decode step with 4 query heads per KV head): the
 //    score products' 16 columns are digit 0, digit 1 and twice digit 2 of the
 //    four, so a lane keeps one of its two tokens and half the softmax work, and
@@ -68,8 +69,6 @@ struct AttnArgs {
 // barrier between warps), across segment ends, the block table's entries a
 // stage ahead of that.
 
-constexpr int kFlush = 16;
-
 // log2(e)
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -78,6 +77,7 @@ struct Cfg {
   static constexpr int D = D_, NT = NT_, TOK = TOK_, WARPS = WARPS_, STAGES = STAGES_;
   static constexpr bool PACK = PACK_, BF16 = BF16_;
   static constexpr int DIGITS = BF16 ? 2 : 3;
+  static constexpr int FLUSH = BF16 ? 256 : 256 / TOK;  // a bf16 output does not notice
   static constexpr int COLS = PACK ? 4 : 8 * NT, GROUPS = TOK / 16;
   // tiles and tokens of a step of the inner loop: four tiles where the registers allow (128K tokens: 42 us; two, 45)
   static constexpr int TILES = NT == 1 && D <= 128 && WARPS == 8 ? 4 : 2, SUB = 16 * TILES;
@@ -855,7 +855,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) attn_paged_kernel(const __gr
       }
 
       const bool ends = cons.tile + 1 == cons.q.stages || u + 1 == count;  // the segment's end, or the run's
-      if (++since == kFlush || (ends && has_flushed)) {
+      if (++since == C::FLUSH || (ends && has_flushed)) {
 #pragma unroll
         for (int k = 0; k < MT; ++k)
 #pragma unroll

@@ -49,6 +49,8 @@ struct LoraArgs {
   int window;  // rows of a window
   int share;   // clusters per window
   int log_blocks;
+  int log_split;  // clusters that share an adapter's outputs, each with an h of its own
+  int few;  // a decode batch
   int vec;  // rows of y and out allow 16-byte accesses
 };
 
@@ -84,11 +86,11 @@ __device__ __forceinline__ void list_rows(const int* ids, int id, int rows, int*
   if (lane == 0) *count = n;
 }
 
-// Rows list[0 .. n) (n <= 16) of adapter id.  Every block of the cluster calls it with the same arguments.  `again`:
-// the blocks' sums of an earlier call may still be read.
+// Rows list[0 .. n) (n <= 16) of adapter id.  Every block of the cluster calls it with the same arguments.  run0: the
+// first of the cluster's runs of outputs, one a block.  `again`: the blocks' sums of an earlier call may still be read.
 template <int KS>
-__device__ void lora_rows(const LoraArgs& P, Shared<KS>& S, const int* list, int n, int row0, int id, bool again,
-                          cg::cluster_group& cluster) {
+__device__ void lora_rows(const LoraArgs& P, Shared<KS>& S, const int* list, int n, int row0, int id, int run0,
+                          bool again, cg::cluster_group& cluster) {
   using C = Shape<KS>;
   const sf_lora_args& a = P.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
@@ -97,8 +99,9 @@ __device__ void lora_rows(const LoraArgs& P, Shared<KS>& S, const int* list, int
 
   // this block's run of groups of 32 output columns
   const uint32_t groups = (a.N + 31u) / 32u;
-  const int g0 = static_cast<int>(static_cast<uint64_t>(groups) * block >> P.log_blocks);
-  const int g1 = static_cast<int>(static_cast<uint64_t>(groups) * (block + 1) >> P.log_blocks);
+  const uint32_t run = run0 + block;
+  const int g0 = static_cast<int>(static_cast<uint64_t>(groups) * run >> (P.log_blocks + P.log_split));
+  const int g1 = static_cast<int>(static_cast<uint64_t>(groups) * (run + 1) >> (P.log_blocks + P.log_split));
   const int r[2] = {g, g + 8};
   const uint16_t* x[2];
   const float* y[2];
@@ -153,7 +156,7 @@ __device__ void lora_rows(const LoraArgs& P, Shared<KS>& S, const int* list, int
     const int r0 = p * C::RB;
     if (p > 0 && r0 >= a.rank) break;
     float acc[C::RB / 8][4] = {};
-#pragma unroll 2
+#pragma unroll 1
     for (int k = 64 * s0; k < 64 * s1; k += 32) {
       const bool in = k + 8 * t < a.K;
       uint4 xv[2], av[C::RB / 8];
@@ -274,7 +277,8 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const __grid_constant
   const sf_lora_args& a = P.a;
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, block = static_cast<int>(cluster.block_rank());
-  const int task = blockIdx.x >> P.log_blocks, window = task / P.share, turn = task % P.share;
+  const int cluster_id = blockIdx.x >> P.log_blocks, run0 = (cluster_id & ((1 << P.log_split) - 1)) << P.log_blocks;
+  const int task = cluster_id >> P.log_split, window = task / P.share, turn = task % P.share;
   const int row0 = window * P.window, rows = min(P.window, a.T - row0);
   if (tid < kMaxWindow) {
     int id = -1;
@@ -308,15 +312,16 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const __grid_constant
     __syncthreads();
     const int n = S.list_n;
     for (int k = 0; k < n; k += kRows) {
-      lora_rows<KS>(P, S, S.list + k, min(kRows, n - k), row0, id, again, cluster);
+      lora_rows<KS>(P, S, S.list + k, min(kRows, n - k), row0, id, run0, again, cluster);
       again = true;
     }
   }
 
   // Rows without an adapter, spread over the window's clusters: four columns, eight rows on their way at once.
   if (a.out != a.y && S.bare_n > turn) {
-    const int p0 = static_cast<int>(static_cast<int64_t>((a.N + 3) / 4) * block >> P.log_blocks);
-    const int p1 = static_cast<int>(static_cast<int64_t>((a.N + 3) / 4) * (block + 1) >> P.log_blocks);
+    const int64_t quads = (a.N + 3) / 4, run = run0 + block;
+    const int p0 = static_cast<int>(quads * run >> (P.log_blocks + P.log_split));
+    const int p1 = static_cast<int>(quads * (run + 1) >> (P.log_blocks + P.log_split));
     const int mine = (S.bare_n - 1 - turn) / P.share + 1;  // rows turn, turn + share, ...
     constexpr int kAhead = 8;
     for (int c = 4 * (p0 + tid); c < 4 * p1; c += 4 * kThreads)
@@ -393,18 +398,26 @@ extern "C" sf_status sf_lora_add(const sf_lora_args* a, sf_stream_t stream) {
   P.a = *a;
   P.vec = sf::aligned(a->out, 16) && a->out_stride % 4 == 0 && (!a->y || (sf::aligned(a->y, 16) && a->y_stride % 4 == 0));
   // Rows of one adapter are found within a window: wide windows for a decode batch, where the adapters' weights are
-  // what is read, narrow ones for prompts, where more of them run at once.
-  P.window = a->T <= 128 ? kMaxWindow : kRows;
+  // what is read, narrow ones for prompts, where more of them run at once.  Only the device knows which it is, so the
+  // rule goes by T (us with windows of 64 / 32 / 16 rows: 256 rows of 16 adapters in any order 22 / 25 / 33; 512 in
+  // runs of 100 rows 31 / 19 / 17).
+  P.few = a->T <= 128;
+  P.window = P.few ? kMaxWindow : a->T <= 512 ? 32 : kRows;
   // Two blocks fit an SM.  Clusters of 8 share a window's adapters while there are few windows; with many windows a
   // cluster is smaller, down to two rounds of blocks: while some sum h, others are at their outputs (2050 rows, rank
-  // 32: 40 us; one round 44, four 48).
+  // 32: 40 us; one round 44, four 48).  Prompts may hold many adapters a window all the same, and a cluster that has
+  // none ends at once: four rounds more of them (36 us; eight, 42).
   const int windows = (a->T - 1) / P.window + 1, room = 2 * sf::sm_count();
   P.log_blocks = 3;
   while (P.log_blocks > 0 && static_cast<int64_t>(windows) << P.log_blocks > 2 * room) --P.log_blocks;
-  P.share = std::max(1, std::min({P.window, a->T, a->n_adapters, (room >> P.log_blocks) / windows}));
-  SF_REQUIRE(static_cast<int64_t>(windows) * P.share << P.log_blocks < (1ll << 31), "%s: T is too large", what);
+  const int most = ((a->T > 512 ? 4 * room : room) >> P.log_blocks) / windows;
+  P.share = std::max(1, std::min({P.window, a->T, a->n_adapters, most}));
+  // A projection's outputs are shared by two clusters while the SMs have room (64 rows, 16 adapters of rank 64, N =
+  // 14336: 24.6 us; one cluster each, 28.1; clusters of 16 blocks instead, 40).
+  P.log_split = P.few && a->N >= 2048 && static_cast<int64_t>(windows) * P.share * 2 << P.log_blocks <= room;
+  SF_REQUIRE(static_cast<int64_t>(windows) * P.share << P.log_blocks < (1ll << 30), "%s: T is too large", what);
   cudaStream_t s = sf::as_cuda(stream);
-  const int clusters = windows * P.share;
+  const int clusters = windows * P.share << P.log_split;
   if (a->rank <= 16) return launch<1>(P, clusters, s);
   if (a->rank <= 32) return launch<2>(P, clusters, s);
   if (a->rank <= 64) return launch<4>(P, clusters, s);
