@@ -392,6 +392,7 @@ extern "C" sf_status sf_lora_add(const sf_lora_args* a, sf_stream_t stream) {
   SF_REQUIRE(a->x && a->A && a->B && a->scale && a->out && (a->ids || a->n_ids == 0), "%s: null pointer", what);
   SF_REQUIRE(a->x_stride >= a->K && a->out_stride >= a->N && (!a->y || a->y_stride >= a->N),
              "%s: a row stride is below the row's length", what);
+  SF_REQUIRE(a->out != a->y || a->out_stride == a->y_stride, "%s: out is y with another row stride", what);
   SF_REQUIRE(sf::aligned(a->A, 16) && sf::aligned(a->B, 16) && sf::aligned(a->x, 16) && a->x_stride % 8 == 0,
              "%s: A, B and the rows of x must be 16-byte aligned", what);
   LoraArgs P{};

@@ -95,7 +95,7 @@ def test_attention_refusals(sf):
                        (dict(scale=float("inf")), "scale"), (dict(out_type=7), "out_type"), (dict(q=None), "null"),
                        (dict(workspace=None), "null"), (dict(q_stride=504), "stride"), (dict(q=264), "aligned"),
                        (dict(q_stride=516), "aligned"), (dict(out_stride=514), "aligned"),
-                       (dict(workspace=264), "aligned"), (dict(ws_bytes=0), "too small")):
+                       (dict(workspace=264), "aligned"), (dict(ws_bytes=0), "too small"), (dict(T=1 << 25), "2^26")):
         _refused(sf, call, args(**bad), match)
     assert call(None, None) == sf.SF_EINVAL
     assert call(ctypes.byref(args(T=0)), None) == sf.SF_OK
@@ -119,7 +119,7 @@ def test_lora_refusals(sf):
                        (dict(N=0), "N >= 1"), (dict(K=0), "K must"), (dict(K=60), "K must"), (dict(rank=0), "rank"),
                        (dict(rank=12), "rank"), (dict(rank=136), "rank"), (dict(x=None), "null"),
                        (dict(ids=None), "null"), (dict(scale=None), "null"), (dict(x_stride=56), "stride"),
-                       (dict(y_stride=39), "stride"), (dict(out_stride=39), "stride"), (dict(A=264), "aligned"),
+                       (dict(y_stride=39), "stride"), (dict(out_stride=39), "stride"), (dict(out_stride=44), "another row stride"), (dict(A=264), "aligned"),
                        (dict(x_stride=68), "aligned"), (dict(x=258), "aligned")):
         _refused(sf, call, args(**bad), match)
     assert call(None, None) == sf.SF_EINVAL

@@ -201,7 +201,9 @@ def _pool_np(kv):
 @pytest.mark.parametrize("T,Hq,Hkv,d,P,src,rope", [
     (1, 32, 8, 128, 64, "fp32", True), (16, 32, 8, 128, 64, "fp32", True), (37, 3, 1, 64, 16, "fp32", True),
     (301, 8, 8, 256, 32, "bf16", True), (5, 0, 2, 128, 16, "fp32", True), (130, 0, 8, 128, 256, "bf16", False),
-    (700, 0, 3, 64, 128, "fp32", False), (2, 0, 256, 64, 16, "fp32", False)])
+    (700, 0, 3, 64, 128, "fp32", False), (2, 0, 256, 64, 16, "fp32", False),
+    # enough rows for a block to take several at a time (4, 8 and 2), odd head counts
+    (2403, 3, 1, 128, 64, "fp32", True), (4801, 1, 1, 64, 64, "bf16", True), (1203, 2, 3, 256, 32, "fp32", True)])
 def test_append(sf, T, Hq, Hkv, d, P, src, rope):
     rng = np.random.default_rng(T + d)
     pages = -(-T // P) + 2
@@ -535,7 +537,8 @@ def _lora_tol(x, A, B, scale, ids, want, K, rank):
 
 @pytest.mark.parametrize("T,K,N,rank,n", [
     (1, 4096, 4096, 16, 3), (16, 4096, 1024, 16, 16), (5, 8, 1, 8, 2), (17, 520, 777, 24, 4), (3, 1000, 130, 128, 3),
-    (64, 512, 1024, 64, 5), (300, 264, 200, 32, 7), (33, 4096, 96, 40, 2), (130, 1032, 4100, 128, 1)])
+    (64, 512, 1024, 64, 5), (300, 264, 200, 32, 7), (33, 4096, 96, 40, 2), (130, 1032, 4100, 128, 1),
+    (700, 72, 520, 16, 5), (128, 64, 3000, 8, 30), (1300, 128, 36, 48, 2)])
 def test_lora(sf, T, K, N, rank, n):
     x, A, B, scale, y = _lora_case(T, K, N, rank, n, T + K)
     rng = np.random.default_rng(T)
@@ -569,6 +572,18 @@ def test_lora_runs_row_of_and_strides(sf):
     sf.lora_add(xs[:, :K], A.cuda(), B.cuda(), scale.cuda(), _i32(per), outs[:, :N], ys[:, :N], row_of=_i32(of))
     tol = _lora_tol(_f64(x), _f64(A), _f64(B), scale.numpy(), ids, want, K, rank)
     assert np.all(np.abs(_f64(outs[:, :N]) - want) <= tol) and torch.all(outs[:, N:] == 7.0)
+
+
+def test_lora_prompts_of_one_adapter(sf):
+    """Whole windows of one adapter, and of none."""
+    T, K, N, rank, n = 900, 320, 260, 32, 4
+    x, A, B, scale, y = _lora_case(T, K, N, rank, n, 4)
+    ids = np.repeat([2, -1, 0, 3, 2], [301, 150, 17, 400, 32])
+    want = osv.lora(_f64(x), _f64(A), _f64(B), scale.numpy(), ids, _f64(y))
+    out = sf.lora_add(x.cuda(), A.cuda(), B.cuda(), scale.cuda(), _i32(ids), torch.full((T, N), 7.0, device="cuda"),
+                      y.cuda())
+    tol = _lora_tol(_f64(x), _f64(A), _f64(B), scale.numpy(), ids, want, K, rank)
+    assert np.all(np.abs(_f64(out) - want) <= tol)
 
 
 def test_lora_nonfinite_stays_in_its_row_and_adapter(sf):
