@@ -4,6 +4,7 @@
 #include <climits>
 #include <cmath>
 
+#include "launch.cuh"
 #include "paged.cuh"
 
 namespace {
@@ -351,7 +352,8 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) attn_paged_kernel(const __gr
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const int group = A.group;
 
-  asm volatile("griddepcontrol.launch_dependents;");  // the join waits for this grid's end
+  sfd::wait_for_previous();
+  sfd::let_next_prepare();
 
   // The units of all requests.
   const int per = (A.R + NTHR - 1) / NTHR;
@@ -996,7 +998,7 @@ __global__ void __launch_bounds__(32 * C::COLS * C::JOIN) attn_paged_join_kernel
   constexpr int D = C::D, Z = (D + 127) / 128;
   __shared__ float sum_sh[C::JOIN][C::COLS];
   __shared__ float4 o_sh[C::JOIN][C::COLS][Z][32];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  sfd::wait_for_previous();
   const Tail tail = W.tails[blockIdx.x];
   if (!tail.open) return;
   const int b = blockIdx.x, n = tail.last_cta - b + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1064,21 +1066,11 @@ struct Kernel {
       SF_CHECK_CUDA(cudaFuncSetAttribute(attn_paged_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
       if (dev < 64) allowed.fetch_or(bit, std::memory_order_relaxed);
     }
-    attn_paged_kernel<C><<<blocks, 32 * C::WARPS, C::SMEM, s>>>(W);
-    sf_status st = sf::check_launch("attn_paged_kernel");
+    sf_status st = sf::launch("attn_paged_kernel", attn_paged_kernel<C>, dim3(blocks), 32 * C::WARPS, C::SMEM, 1, s, W);
     if (st != SF_OK) return st;
-    // launched while the first kernel runs; its blocks start as that one's end, and wait for the last
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(blocks);
-    cfg.blockDim = dim3(32 * C::COLS * C::JOIN);
-    cfg.stream = s;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    SF_CHECK_CUDA(cudaLaunchKernelEx(&cfg, attn_paged_join_kernel<C>, W));
-    return sf::check_launch("attn_paged_join_kernel");
+    // its blocks start as the first kernel's end, and wait for the last
+    return sf::launch("attn_paged_join_kernel", attn_paged_join_kernel<C>, dim3(blocks), 32 * C::COLS * C::JOIN, 0, 1,
+                      s, W);
   }
 };
 

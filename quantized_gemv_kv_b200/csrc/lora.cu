@@ -24,6 +24,7 @@
 
 #include <cooperative_groups.h>
 
+#include "launch.cuh"
 #include "sf_internal.h"
 
 namespace {
@@ -272,6 +273,7 @@ __device__ void lora_rows(const LoraArgs& P, Shared<KS>& S, const int* list, int
 
 template <int KS>
 __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const __grid_constant__ LoraArgs P) {
+  sfd::wait_for_previous();
   extern __shared__ __align__(16) unsigned char smem[];
   Shared<KS>& S = *reinterpret_cast<Shared<KS>*>(smem);
   const sf_lora_args& a = P.a;
@@ -358,24 +360,13 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const __grid_constant
 }
 
 template <int KS>
-sf_status launch(const LoraArgs& P, int clusters, cudaStream_t s) {
+sf_status launch_lora(const LoraArgs& P, int clusters, cudaStream_t s) {
   const size_t smem = sizeof(Shared<KS>);
   if (smem > 48 * 1024)
     SF_CHECK_CUDA(
         cudaFuncSetAttribute(lora_kernel<KS>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(clusters << P.log_blocks);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = 1 << P.log_blocks;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  SF_CHECK_CUDA(cudaLaunchKernelEx(&cfg, lora_kernel<KS>, P));
-  return sf::check_launch("lora_kernel");
+  return sf::launch("lora_kernel", lora_kernel<KS>, dim3(clusters << P.log_blocks), kThreads, smem, 1 << P.log_blocks, s,
+                    P);
 }
 
 }  // namespace
@@ -419,8 +410,8 @@ extern "C" sf_status sf_lora_add(const sf_lora_args* a, sf_stream_t stream) {
   SF_REQUIRE(static_cast<int64_t>(windows) * P.share << P.log_blocks < (1ll << 30), "%s: T is too large", what);
   cudaStream_t s = sf::as_cuda(stream);
   const int clusters = windows * P.share << P.log_split;
-  if (a->rank <= 16) return launch<1>(P, clusters, s);
-  if (a->rank <= 32) return launch<2>(P, clusters, s);
-  if (a->rank <= 64) return launch<4>(P, clusters, s);
-  return launch<8>(P, clusters, s);
+  if (a->rank <= 16) return launch_lora<1>(P, clusters, s);
+  if (a->rank <= 32) return launch_lora<2>(P, clusters, s);
+  if (a->rank <= 64) return launch_lora<4>(P, clusters, s);
+  return launch_lora<8>(P, clusters, s);
 }

@@ -5,6 +5,7 @@
 
 #include <cooperative_groups.h>
 
+#include "launch.cuh"
 #include "paged.cuh"
 #include "produce.cuh"
 
@@ -53,6 +54,7 @@ __device__ __forceinline__ int owner_of(const int* cum, int R, int v) {
 constexpr int kPlanArrays = 5;
 
 __global__ void __launch_bounds__(512) paged_plan_kernel(const __grid_constant__ PlanArgs P) {
+  sfd::wait_for_previous();
   extern __shared__ int sh[];
   const sf_paged_plan_args& a = P.a;
   const int R = a.R, shift = P.shift, tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
@@ -304,6 +306,7 @@ __global__ void __launch_bounds__(32 * kAppWarps) paged_append_kernel(const __gr
   __shared__ double freq[H];
   __shared__ double2 turn[2][MAX_ROWS][H];  // cosine, sine; two groups, so that one barrier a group does
   __shared__ float2 turn32[2][MAX_ROWS][H];
+  sfd::wait_for_previous();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool rot = A.theta > 0.0;
   if (rot && tid < H) freq[tid] = pow(A.theta, -2.0 * tid / D);
@@ -492,13 +495,12 @@ __global__ void __launch_bounds__(32 * kAppWarps) paged_append_kernel(const __gr
 }
 
 template <typename S>
-void launch_append(const AppendArgs& A, int d, dim3 grid, cudaStream_t s) {
-  if (d == 64)
-    paged_append_kernel<64, S><<<grid, 32 * kAppWarps, 0, s>>>(A);
-  else if (d == 128)
-    paged_append_kernel<128, S><<<grid, 32 * kAppWarps, 0, s>>>(A);
-  else
-    paged_append_kernel<256, S><<<grid, 32 * kAppWarps, 0, s>>>(A);
+sf_status launch_append(const AppendArgs& A, int d, dim3 grid, cudaStream_t s) {
+  return sf::launch("paged_append_kernel",
+                    d == 64    ? paged_append_kernel<64, S>
+                    : d == 128 ? paged_append_kernel<128, S>
+                               : paged_append_kernel<256, S>,
+                    grid, 32 * kAppWarps, 0, 1, s, A);
 }
 
 }  // namespace
@@ -525,21 +527,10 @@ extern "C" sf_status sf_paged_plan(const sf_paged_plan_args* a, sf_stream_t stre
   if (smem > 48 * 1024)
     SF_CHECK_CUDA(cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem)));
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(blocks);
-  cfg.blockDim = dim3(small ? 128 : 512);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = sf::as_cuda(stream);
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = blocks;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
   if (blocks > 8)
     SF_CHECK_CUDA(cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
-  SF_CHECK_CUDA(cudaLaunchKernelEx(&cfg, paged_plan_kernel, P));
-  return sf::check_launch("paged_plan_kernel");
+  return sf::launch("paged_plan_kernel", paged_plan_kernel, dim3(blocks), small ? 128 : 512, smem, blocks,
+                    sf::as_cuda(stream), P);
 }
 
 extern "C" sf_status sf_paged_append(const sf_paged_append_args* a, sf_stream_t stream) {
@@ -603,9 +594,7 @@ extern "C" sf_status sf_paged_append(const sf_paged_append_args* a, sf_stream_t 
   const int need = ((kv.Hkv + 1) / 2 * 2 + (a->Hq + 1) / 2 + kAppWarps - 1) / kAppWarps;  // blocks that one row can fill
   const int gx = std::min((a->T - 1) / A.group + 1, sms * 8);
   const int gy = std::max(1, std::min(need, sms * 2 / gx));
-  if (a->src_type == SF_F32)
-    launch_append<float>(A, kv.d, dim3(gx, gy), sf::as_cuda(stream));
-  else
-    launch_append<uint16_t>(A, kv.d, dim3(gx, gy), sf::as_cuda(stream));
-  return sf::check_launch("paged_append_kernel");
+  const dim3 grid(gx, gy);
+  return a->src_type == SF_F32 ? launch_append<float>(A, kv.d, grid, sf::as_cuda(stream))
+                               : launch_append<uint16_t>(A, kv.d, grid, sf::as_cuda(stream));
 }
