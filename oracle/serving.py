@@ -106,7 +106,7 @@ def attention(q: np.ndarray, k_pool: np.ndarray, v_pool: np.ndarray, cu, lens, t
         pg, off = (np.array([a[c] for a in at], dtype=np.int64) for c in (0, 1))
         toks = np.array(toks, dtype=np.int64)
         for r in rows:
-            p = n - (cu[i + 1] - cu[i]) + (r - cu[i])
+            p = int(n - (cu[i + 1] - cu[i]) + (r - cu[i]))
             see = (toks <= p) & ((toks > p - window) if window > 0 else True)
             for h in range(Hkv):
                 if not see.any():

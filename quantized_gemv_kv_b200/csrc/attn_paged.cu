@@ -51,8 +51,8 @@ struct AttnArgs {
 //    largest seen); movmatrix turns them from score order to operand order.  The
 //    tensor cores truncate their fp32 sums, so a chain of them drifts (7e-6 over
 //    a run of 112): after FLUSH stages the sums are added, rounded, to sums in
-//    shared memory and start again (128K tokens: 1.4e-6 off with four stages for
-//    45.8 us, 4.4e-6 with none for 45.0; sums in the workspace cost 20%);
+//    shared memory and start again (128K tokens: 1.4e-6 off with four stages,
+//    4.4e-6 with none in 2% less time; sums in the workspace cost 20%);
 //  * PACK, up to 4 columns (a decode step with 4 query heads per KV head): the
 //    score products' 16 columns are digit 0, digit 1 and twice digit 2 of the
 //    four, so a lane keeps one of its two tokens and half the softmax work, and
@@ -202,6 +202,11 @@ __device__ __forceinline__ int row_of(const AttnArgs& A, int c) {
   return A.per_group == 0 ? c : static_cast<int>(__umulhi(static_cast<uint32_t>(c), A.per_group));
 }
 
+// The first token that the row at position p sees; p may be negative, and the window as long as an int can say.
+__device__ __forceinline__ int window_begin(const AttnArgs& A, int p) {
+  return A.window > 0 && p >= A.window ? p - A.window + 1 : 0;
+}
+
 // One request's columns and stages.
 struct Req {
   int row0, rows;    // its rows in q and out (those below T)
@@ -221,8 +226,8 @@ __device__ __forceinline__ Req load_req(const AttnArgs& A, int i) {
   q.len = min(max(A.len[i], 0), A.max_pages << A.shift);
   q.end = max(q.len - (q.last - (q.row0 + q.rows)), 0);
   const int first = q.len - (q.last - q.row0);  // the first row's position
-  q.st0 = A.window > 0 ? max(first - A.window + 1, 0) / C::TOK : 0;
-  q.stages = max((q.end + C::TOK - 1) / C::TOK - q.st0, 1);
+  q.st0 = window_begin(A, first) / C::TOK;
+  q.stages = max((q.end - 1) / C::TOK + 1 - q.st0, 1);
   q.blocks = (q.rows * A.group + C::COLS - 1) / C::COLS;
   return q;
 }
@@ -586,7 +591,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) attn_paged_kernel(const __gr
             const int cc = c0 + 8 * n + col0 + z;
             const int p = cons.q.len - (cons.q.last - (cons.q.row0 + row_of(A, cc)));
             lim_hi[n][z] = cc < cols ? p + 1 : INT_MAX;
-            lim_lo[n][z] = cc < cols && A.window > 0 ? p + 1 - A.window : INT_MIN;
+            lim_lo[n][z] = cc < cols ? window_begin(A, p) : 0;
             m[n][z] = -INFINITY;
             l[n][z] = zs[n][z] = 0.f;
           }
@@ -595,8 +600,8 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) attn_paged_kernel(const __gr
         const int r_last = cons.q.row0 + row_of(A, min(c0 + C::COLS, cols) - 1);
         all_hi = cons.q.len - (cons.q.last - r_first) + 1;
         any_hi = cons.q.len - (cons.q.last - r_last) + 1;
-        all_lo = A.window > 0 ? any_hi - A.window : 0;
-        any_lo = A.window > 0 ? all_hi - A.window : 0;
+        all_lo = window_begin(A, any_hi - 1);
+        any_lo = window_begin(A, all_hi - 1);
 #pragma unroll
         for (int s = 0; s < MT; ++s)
 #pragma unroll
@@ -614,7 +619,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) attn_paged_kernel(const __gr
       }
       const unsigned char* stage = ring + slot * C::STAGEB;
       if (++slot == C::STAGES) slot = 0;
-      // Two tiles at a time; kept a loop, since a stage's whole code is more than the instruction cache likes.
+      // TILES tiles at a time; kept a loop, since a stage's whole code is more than the instruction cache likes.
 #pragma unroll 1
       for (int sub = 0; sub < TOK / C::SUB; ++sub) {
       const unsigned char* st = stage + sub * TILES * C::TILEB;
@@ -625,7 +630,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) attn_paged_kernel(const __gr
       bool odd = false;
 #pragma unroll
       for (int z = 0; z < C::SUB; z += 32) odd |= (kpar[z + lane] & 0xFFFFu) == 0;
-      odd = __any_sync(0xffffffffu, odd) || tok0 + C::SUB > all_hi || tok0 < all_lo;
+      odd = __any_sync(0xffffffffu, odd) || tok0 > all_hi - C::SUB || tok0 < all_lo;
 
       // scores in base 2: tokens tok_of[k] x columns col0, col0 + 1
       float s[TILES][NT][ROWS][2];

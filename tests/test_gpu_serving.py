@@ -480,6 +480,32 @@ def test_attention_rows_behind_the_buffer(sf):
     assert torch.all(got[0] == 0.0) and torch.isfinite(out).all()
 
 
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 3])
+def test_attention_window_longer_than_any_request(sf, window):
+    """The largest windows beside requests of more rows than tokens."""
+    c = _Case(sf, 53, [5, 3, 1], [1, 90, 0], 8, 2, 128, 16)
+    c.check(sf, window=window)
+    assert torch.equal(c.run(sf, window=window), c.run(sf))
+
+
+def test_attention_longest_table(sf):
+    """A table of 2^31 - 16 tokens, the most there can be: one page in its first half, another in its second, a third
+    one for the last 11 tokens, which change nothing that counts here (2^-24)."""
+    d, P, n = 64, 16, 2 ** 27 - 1
+    c = _Case(sf, 59, [1, 1, 1], [16, 16, 16], 1, 1, d, P, extra_rows=0)
+    a, b, last = (int(c.table[i, 0]) for i in range(3))
+    table = torch.full((1, n), a, dtype=torch.int32, device="cuda")
+    table[0, n // 2:] = b
+    table[0, -1] = last
+    got = _f64(sf.attn_paged(c.q[:1].cuda(), c.kv, _i32([0, 1]), _i32([n * P - 5]), table))[0]
+    k, v = (np.concatenate([c.val[w, a, 0], c.val[w, b, 0]]) for w in (0, 1))
+    s = _f64(c.q)[0] @ k.T / np.sqrt(d)
+    w = np.exp(s - s.max(-1, keepdims=True))
+    want = (w / w.sum(-1, keepdims=True)) @ v
+    # a lane sums the weights of up to 2^31 / (148 * 8 * 8) = 226722 tokens one by one: 2^-24 of the sum each
+    assert np.abs(got - want).max() <= np.abs(v).max() * 226722 * 2.0 ** -23
+
+
 def test_attention_repeats_bit_for_bit(sf):
     c = _Case(sf, 43, [1, 2, 1], [9000, 64, 1200], 8, 2, 128, 64)
     first = c.run(sf)
