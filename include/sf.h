@@ -769,7 +769,9 @@ typedef enum sf_dtype { SF_F32 = 0, SF_BF16 = 1 } sf_dtype;
  *           the low half and fp16 zero point in the high half; a key scale
  *           whose bits are 0 marks a token that does not exist.
  * Quantizer: sf_quantize_nested's with b = 4 and one group of d values per
- * token-head; the value of code c is scale * (c - zero).
+ * token-head; the value of code c is scale * (c - zero).  Scales and zero points
+ * of tokens that some row of a step attends to are finite (sf_paged_append
+ * writes no others); whatever else the pool holds changes nothing.
  * page_rows: token-head rows from one page to the next in all four arrays
  * (pages of several layers interleaved in one allocation); 0 means
  * Hkv * page_size, otherwise at least that and a multiple of 4.
@@ -813,7 +815,7 @@ typedef struct sf_paged_kv {
  * Apart from the two pairs named, outputs must not overlap inputs.
  * Constraints: 1 <= R <= 8192, page_size a power of two in [16, 256],
  *   max_pages >= 1, max_pages * page_size < 2^31, table_stride >= max_pages,
- *   max_rows >= 1, free_cap >= 1.
+ *   max_rows and free_cap in [1, 2^30].
  */
 enum { SF_PLAN_OK = 0, SF_PLAN_LENGTH = 1, SF_PLAN_ROWS = 2, SF_PLAN_PAGES = 3 };
 typedef struct sf_paged_plan_args {
@@ -914,8 +916,8 @@ sf_status sf_attn_paged(const sf_attn_paged_args* a, sf_stream_t stream);
  * An adapter of a smaller rank is padded with zero rows of A.
  * A x is kept in fp32 (it enters the second product as three bf16 terms, 24
  * bits); all sums are fp32 in a fixed order.
- * Constraints: T >= 0, n_ids >= 0, n_adapters >= 1, N >= 1, K a positive
- *   multiple of 8, rank a multiple of 8 in [8, 128]; A, B 16-byte aligned, rows
+ * Constraints: T >= 0, n_ids >= 0, n_adapters >= 1, N in [1, 2^30], K a positive
+ *   multiple of 8 up to 2^30, rank a multiple of 8 in [8, 128]; A, B 16-byte aligned, rows
  *   of x 16-byte aligned, strides at least a row.
  */
 typedef struct sf_lora_args {

@@ -515,7 +515,9 @@ extern "C" sf_status sf_paged_plan(const sf_paged_plan_args* a, sf_stream_t stre
   SF_REQUIRE(a->max_pages >= 1 && static_cast<int64_t>(a->max_pages) * a->page_size < (1ll << 31),
              "sf_paged_plan: need max_pages >= 1 and max_pages * page_size < 2^31");
   SF_REQUIRE(a->table_stride >= a->max_pages, "sf_paged_plan: table_stride is below max_pages");
-  SF_REQUIRE(a->max_rows >= 1 && a->free_cap >= 1, "sf_paged_plan: need max_rows >= 1 and free_cap >= 1");
+  // (the loops' indexes run past the two by less than that)
+  SF_REQUIRE(a->max_rows >= 1 && a->free_cap >= 1 && a->max_rows <= 1 << 30 && a->free_cap <= 1 << 30,
+             "sf_paged_plan: max_rows and free_cap must be in [1, 2^30]");
   PlanArgs P{*a, sf::log2i(a->page_size),
              sf::aligned(a->slots, 16) && sf::aligned(a->positions, 16) && sf::aligned(a->row_request, 16),
              a->max_rows > 4096 ? 4 : 1};

@@ -47,7 +47,8 @@ def test_plan_refusals(sf):
     for bad, match in ((dict(len=None), "null"), (dict(status=None), "null"), (dict(R=0), "R must"),
                        (dict(R=8193), "R must"), (dict(page_size=20), "page_size"), (dict(max_pages=0), "max_pages"),
                        (dict(max_pages=1 << 27, table_stride=1 << 27), "max_pages"), (dict(table_stride=3), "stride"),
-                       (dict(max_rows=0), "max_rows"), (dict(free_cap=0), "free_cap")):
+                       (dict(max_rows=0), "max_rows"), (dict(free_cap=0), "free_cap"),
+                       (dict(max_rows=2 ** 30 + 1), "max_rows"), (dict(free_cap=2 ** 31 - 1), "free_cap")):
         _refused(sf, sf._lib.sf_paged_plan, _PlanArgs(*{**good, **bad}.values()), match)
     assert sf._lib.sf_paged_plan(None, None) == sf.SF_EINVAL
 
@@ -117,6 +118,7 @@ def test_lora_refusals(sf):
     call = sf._lib.sf_lora_add
     for bad, match in ((dict(T=-1), "T >= 0"), (dict(n_ids=-1), "n_ids"), (dict(n_adapters=0), "n_adapters"),
                        (dict(N=0), "N >= 1"), (dict(K=0), "K must"), (dict(K=60), "K must"), (dict(rank=0), "rank"),
+                       (dict(N=2 ** 30 + 1), "N <= 2^30"), (dict(K=2 ** 31 - 8), "K must"),
                        (dict(rank=12), "rank"), (dict(rank=136), "rank"), (dict(x=None), "null"),
                        (dict(ids=None), "null"), (dict(scale=None), "null"), (dict(x_stride=56), "stride"),
                        (dict(y_stride=39), "stride"), (dict(out_stride=39), "stride"), (dict(out_stride=44), "another row stride"), (dict(A=264), "aligned"),

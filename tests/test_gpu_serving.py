@@ -627,6 +627,20 @@ def test_lora_nonfinite_stays_in_its_row_and_adapter(sf):
     assert torch.equal(out[ok], clean[ok]) and torch.isnan(out[4]).all()
 
 
+@pytest.mark.parametrize("rank", [8, 24, 72])
+def test_lora_infinite_inputs(sf, rank):
+    """An infinite A x gives what the formula gives: infinities of B's signs, NaN where they cancel."""
+    x, A, B, scale, y = _lora_case(3, 64, 40, rank, 1, 9)
+    A, B = A.abs() + 1.0, B.abs() + 1.0
+    B[0, 7], B[0, 9, 2] = -B[0, 7], -1.0
+    x[1, 9], x[2, 3], x[2, 50] = float("-inf"), float("inf"), float("-inf")
+    out = _f64(sf.lora_add(x.cuda(), A.cuda(), B.cuda(), scale.cuda(), _i32([0, 0, 0]), y=y.cuda()))
+    want = np.full(40, -np.inf)
+    want[7], want[9] = np.inf, np.nan
+    assert np.isfinite(out[0]).all() and np.isnan(out[2]).all()
+    np.testing.assert_array_equal(out[1], want)
+
+
 def test_lora_repeats_bit_for_bit_in_a_graph(sf):
     T, K, N, rank, n = 24, 2048, 1000, 16, 6
     x, A, B, scale, y = _lora_case(T, K, N, rank, n, 6)
