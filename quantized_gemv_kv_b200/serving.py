@@ -11,6 +11,7 @@ devices and strides are checked here, everything else by the library.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 from dataclasses import dataclass
@@ -122,7 +123,9 @@ class _Job:
 
     def run(self, stream: torch.cuda.Stream | None = None) -> None:
         """Enqueues the call on ``stream`` (default: the current stream of
-        the tensors' device)."""
+        the tensors' device).  What the object allocated belongs to the
+        stream that was current then: order ``stream`` behind it, and keep
+        the object until the call's work has ended."""
         if stream is None:
             raw = _raw_stream(self._index)  # torch.cuda.current_stream().cuda_stream, without the Stream object
         elif stream.device != self.device:
@@ -136,6 +139,11 @@ class _Job:
                 status = self._call(self._ref, raw)
         if status:
             _check(status)
+
+
+def _on(stream: torch.cuda.Stream | None):
+    """What is allocated inside belongs to the stream that the call runs on."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 # ---- the pool ------------------------------------------------------------------
@@ -235,8 +243,9 @@ class PagedPlan(_Job):
 def paged_plan(lens, add, block_table, free_list, n_free, page_size, max_rows, keep=None, lens_out=None,
                n_free_out=None, stream=None) -> PagedPlan:
     """One ``sf_paged_plan`` call; returns the ``PagedPlan`` with its outputs."""
-    job = PagedPlan(lens, add, block_table, free_list, n_free, page_size, max_rows, keep, lens_out, n_free_out)
-    job.run(stream)
+    with _on(stream):
+        job = PagedPlan(lens, add, block_table, free_list, n_free, page_size, max_rows, keep, lens_out, n_free_out)
+        job.run(stream)
     return job
 
 
@@ -297,8 +306,9 @@ class PagedAppend(_Job):
 def paged_append(kv, k, v, slots, positions=None, theta=0.0, q=None, q_out=None, k_val=None, v_val=None,
                  stream=None) -> torch.Tensor | None:
     """One ``sf_paged_append`` call; returns q_out (None without q)."""
-    job = PagedAppend(kv, k, v, slots, positions, theta, q, q_out, k_val, v_val)
-    job.run(stream)
+    with _on(stream):
+        job = PagedAppend(kv, k, v, slots, positions, theta, q, q_out, k_val, v_val)
+        job.run(stream)
     return job.q_out
 
 
@@ -358,8 +368,9 @@ class PagedAttention(_Job):
 def attn_paged(q, kv, cu_rows, lens, block_table, out=None, scale=None, window=0, workspace=None,
                stream=None) -> torch.Tensor:
     """One ``sf_attn_paged`` call; returns out."""
-    job = PagedAttention(q, kv, cu_rows, lens, block_table, out, scale, window, workspace)
-    job.run(stream)
+    with _on(stream):
+        job = PagedAttention(q, kv, cu_rows, lens, block_table, out, scale, window, workspace)
+        job.run(stream)
     return job.out
 
 
@@ -409,6 +420,7 @@ class LoraAdd(_Job):
 
 def lora_add(x, A, B, scale, ids, out=None, y=None, row_of=None, stream=None) -> torch.Tensor:
     """One ``sf_lora_add`` call; returns out."""
-    job = LoraAdd(x, A, B, scale, ids, out, y, row_of)
-    job.run(stream)
+    with _on(stream):
+        job = LoraAdd(x, A, B, scale, ids, out, y, row_of)
+        job.run(stream)
     return job.out

@@ -544,6 +544,29 @@ def test_attention_in_graphs_and_on_other_streams(sf):
             assert torch.equal(out[:rows], c.run(sf)[:rows])
 
 
+def test_functions_on_another_stream(sf):
+    """A function allocates on the stream it is given: nothing that the current stream does with its memory meantime
+    gets in the way, and the zeros of an output come before the call."""
+    c = _Case(sf, 61, [1, 2], [4000, 300], 8, 2, 128, 64)
+    q, cu, lens, table = c.q.cuda(), _i32(c.cu), _i32(c.lens), _i32(c.table)
+    want = sf.attn_paged(q, c.kv, cu, lens, table)
+    x, A, B, scale, _ = _lora_case(5, 128, 96, 8, 2, 62)
+    args = [t.cuda() for t in (x, A, B, scale)] + [_i32([0, 1, 0, -1, 1])]
+    add = sf.lora_add(*args)
+    torch.cuda.synchronize()
+    need = sf.attn_paged_workspace_size(c.T, 2, 8, 2, 128)
+    s = torch.cuda.Stream()
+    for _ in range(3):
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(5_000_000)
+        out, got = sf.attn_paged(q, c.kv, cu, lens, table, stream=s), sf.lora_add(*args, stream=s)
+        for _ in range(20):
+            torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+            torch.full(want.shape, 9.0, device="cuda")
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(got, add)
+
+
 # ---- adapters --------------------------------------------------------------------
 
 
