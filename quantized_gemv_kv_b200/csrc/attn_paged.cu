@@ -51,8 +51,9 @@ struct AttnArgs {
 //    largest seen); movmatrix turns them from score order to operand order.  The
 //    tensor cores truncate their fp32 sums, so a chain of them drifts (7e-6 over
 //    a run of 112): after FLUSH stages the sums are added, rounded, to sums in
-//    shared memory and start again (128K tokens: 1.4e-6 off with four stages,
-//    4.4e-6 with none in 2% less time; sums in the workspace cost 20%);
+//    shared memory and start again (128K tokens: 0.8e-6 off with a flush every 64
+//    tokens; every 256 in 3% less time, 1.4e-6; none in 5% less, 4.4e-6; sums in
+//    the workspace instead cost 20%);
 //  * PACK, up to 4 columns (a decode step with 4 query heads per KV head): the
 //    score products' 16 columns are digit 0, digit 1 and twice digit 2 of the
 //    four, so a lane keeps one of its two tokens and half the softmax work, and
@@ -78,7 +79,7 @@ struct Cfg {
   static constexpr int D = D_, NT = NT_, TOK = TOK_, WARPS = WARPS_, STAGES = STAGES_;
   static constexpr bool PACK = PACK_, BF16 = BF16_;
   static constexpr int DIGITS = BF16 ? 2 : 3;
-  static constexpr int FLUSH = BF16 ? 256 : 256 / TOK;  // a bf16 output does not notice
+  static constexpr int FLUSH = BF16 ? 256 : 64 / TOK;  // a bf16 output does not notice
   static constexpr int COLS = PACK ? 4 : 8 * NT, GROUPS = TOK / 16;
   // tiles and tokens of a step of the inner loop: four tiles where the registers allow (128K tokens: 42 us; two, 45)
   static constexpr int TILES = NT == 1 && D <= 128 && WARPS == 8 ? 4 : 2, SUB = 16 * TILES;
@@ -494,7 +495,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) attn_paged_kernel(const __gr
     int all_hi = 0, all_lo = 0;  // tokens in [all_lo, all_hi) are seen by every column
     int any_hi = 0, any_lo = 0;  // those outside [any_lo, any_hi) by none
     float acc[MT][NT][4];  // the value sums since the last flush
-    float* const flushed = reinterpret_cast<float*>(smem + C::WARPS * C::RINGB) + warp * C::SUMS + lane;
+    float4* const flushed = reinterpret_cast<float4*>(smem + C::WARPS * C::RINGB) + warp * (C::SUMS / 4) + lane;
     int since = 0;         // stages in acc
     bool has_flushed = false, empty = true;  // empty: nothing in acc yet
     float vscale = 0.f;  // power of two that the value scales are multiplied by
@@ -779,9 +780,11 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) attn_paged_kernel(const __gr
 #pragma unroll 1
           for (int k = 0; k < MT; ++k)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int z = 0; z < 4; ++z) flushed[((k * NT + n) * 4 + z) * 32] *= alpha[n][z & 1];
+            for (int n = 0; n < NT; ++n) {
+              float4& f = flushed[(k * NT + n) * 32];
+              const float4 x = f;
+              f = make_float4(x.x * alpha[n][0], x.y * alpha[n][1], x.z * alpha[n][0], x.w * alpha[n][1]);
+            }
         }
         }
       }
@@ -866,14 +869,18 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) attn_paged_kernel(const __gr
 #pragma unroll
         for (int k = 0; k < MT; ++k)
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int z = 0; z < 4; ++z) {
-              float* f = flushed + ((k * NT + n) * 4 + z) * 32;
-              if (has_flushed) acc[k][n][z] += *f;
-              *f = acc[k][n][z];
-              if (!ends) acc[k][n][z] = 0.f;
+          for (int n = 0; n < NT; ++n) {
+            float4& f = flushed[(k * NT + n) * 32];
+            float(&x)[4] = acc[k][n];
+            if (has_flushed) {
+              const float4 y = f;
+              x[0] += y.x, x[1] += y.y, x[2] += y.z, x[3] += y.w;
             }
+            if (!ends) {
+              f = make_float4(x[0], x[1], x[2], x[3]);
+              x[0] = x[1] = x[2] = x[3] = 0.f;
+            }
+          }
         since = 0;
         has_flushed = true;
       }
