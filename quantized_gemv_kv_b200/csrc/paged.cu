@@ -1,6 +1,7 @@
 // The step's bookkeeping for a paged 4-bit KV cache (sf_paged_plan) and the
 // append of its rows (sf_paged_append).
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include <cooperative_groups.h>
@@ -335,8 +336,13 @@ __global__ void __launch_bounds__(32 * kAppWarps) paged_append_kernel(const __gr
         load_row<NP, S>(src + k * stride + H, next_hi[k]);
       }
     };
+    // a warp takes every step-th (unit, kAhead rows) of the group, the units of the first rows first
     int u = blockIdx.y * kAppWarps + warp, k0 = 0;
-    if (u < units) load(u, 0);
+    auto wrap = [&]() {
+      for (; u >= units && k0 < rows; u -= units) k0 += kAhead;
+    };
+    wrap();
+    if (k0 < rows) load(u, k0);
     if (rot) {
       if (tid < rows * H) {
         double s, c;
@@ -346,7 +352,7 @@ __global__ void __launch_bounds__(32 * kAppWarps) paged_append_kernel(const __gr
       }
       __syncthreads();
     }
-    while (u < units) {
+    while (k0 < rows) {
       float lo[kAhead][NP], hi[kAhead][NP];
       int slots[kAhead];
 #pragma unroll
@@ -361,12 +367,9 @@ __global__ void __launch_bounds__(32 * kAppWarps) paged_append_kernel(const __gr
       const int kind = u < kv_pairs ? 0 : u < 2 * kv_pairs ? 1 : 2;  // keys, values, queries
       const int h = 2 * (u - kind * kv_pairs) + half, row_k = k0;
       const bool in = h < (kind == 2 ? A.Hq : A.Hkv);  // an odd number of heads leaves half a warp over
-      k0 += kAhead;
-      if (k0 >= rows) {
-        k0 = 0;
-        u += step;
-      }
-      if (u < units) load(u, k0);
+      u += step;
+      wrap();
+      if (k0 < rows) load(u, k0);
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
         const int slot = slots[k], row = row_k + k;
@@ -494,13 +497,11 @@ __global__ void __launch_bounds__(32 * kAppWarps) paged_append_kernel(const __gr
   }
 }
 
+using AppendKernel = void (*)(AppendArgs);
+
 template <typename S>
-sf_status launch_append(const AppendArgs& A, int d, dim3 grid, cudaStream_t s) {
-  return sf::launch("paged_append_kernel",
-                    d == 64    ? paged_append_kernel<64, S>
-                    : d == 128 ? paged_append_kernel<128, S>
-                               : paged_append_kernel<256, S>,
-                    grid, 32 * kAppWarps, 0, 1, s, A);
+AppendKernel append_kernel(int d) {
+  return d == 64 ? paged_append_kernel<64, S> : d == 128 ? paged_append_kernel<128, S> : paged_append_kernel<256, S>;
 }
 
 }  // namespace
@@ -589,14 +590,24 @@ extern "C" sf_status sf_paged_append(const sf_paged_append_args* a, sf_stream_t 
   A.Hkv = kv.Hkv;
   A.shift = sf::log2i(kv.page_size);
   A.slot_end = kv.num_pages * kv.page_size;
-  // Few rows: a row's heads are spread over blocks until the SMs are filled.  Many rows: a block keeps all heads of a
-  // group of rows (as many as its threads have sines for) and loops over groups.
-  const int sms = sf::sm_count(), most = 64 * kAppWarps / kv.d;
-  A.group = a->T >= 4 * sms * most ? most : 1;
+  // One round of blocks that fit the SMs.  Few rows: a row's heads are spread over blocks.  Many rows: a block keeps
+  // all heads of a group of rows (as many as its threads have sines for, as few as make one round, an even number
+  // where a warp takes two at a time) and loops over groups, so that what a block does once is done less often (us; one
+  // row a group and blocks for two or three rounds: 1000 rows of 40 rotated heads of 128, 11.2 / 13.3; 1000 of 12 of
+  // 64, 4.7 / 5.9).
+  const AppendKernel kernel = a->src_type == SF_F32 ? append_kernel<float>(kv.d) : append_kernel<uint16_t>(kv.d);
+  static std::atomic<int> fits[2][3];  // the kernels' blocks on an SM, once asked for
+  std::atomic<int>& known = fits[a->src_type == SF_F32][kv.d / 128];
+  int fit = known.load(std::memory_order_relaxed);
+  if (fit == 0) {
+    SF_CHECK_CUDA(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, 32 * kAppWarps, 0));
+    known.store(fit, std::memory_order_relaxed);
+  }
+  const int sms = sf::sm_count(), room = sms * std::max(fit, 1), most = 64 * kAppWarps / kv.d;
+  A.group = std::min(most, (a->T - 1) / room + 1);
+  if (A.group > 1 && kv.d < 256) A.group += A.group % 2;
   const int need = ((kv.Hkv + 1) / 2 * 2 + (a->Hq + 1) / 2 + kAppWarps - 1) / kAppWarps;  // blocks that one row can fill
-  const int gx = std::min((a->T - 1) / A.group + 1, sms * 8);
+  const int gx = std::min((a->T - 1) / A.group + 1, room);
   const int gy = std::max(1, std::min(need, sms * 2 / gx));
-  const dim3 grid(gx, gy);
-  return a->src_type == SF_F32 ? launch_append<float>(A, kv.d, grid, sf::as_cuda(stream))
-                               : launch_append<uint16_t>(A, kv.d, grid, sf::as_cuda(stream));
+  return sf::launch("paged_append_kernel", kernel, dim3(gx, gy), 32 * kAppWarps, 0, 1, sf::as_cuda(stream), A);
 }
