@@ -683,6 +683,50 @@ def test_lora_repeats_bit_for_bit_in_a_graph(sf):
         assert torch.equal(out, first)
 
 
+def test_lora_forks_and_joins_in_a_graph(sf):
+    """Calls of two streams that wait for one another, eager and captured: each sees what both streams wrote before it."""
+    T, K, N, rank, n = 16, 512, 512, 16, 4
+    x, A, B, scale, y = _lora_case(T, K, N, rank, n, 8)
+    ids = _i32(np.arange(T) % n)
+    A, B, scale = A.cuda(), B.cuda(), scale.cuda()
+    x, y0, y1, y2 = x.cuda(), y.cuda(), torch.empty((T, N), device="cuda"), torch.empty((T, N), device="cuda")
+    x1, x2 = torch.empty_like(x), torch.empty_like(x)
+    first, left, right, last = (sf.LoraAdd(a, A, B, scale, ids, out, src) for a, out, src in
+                                ((x, y1, y0), (x1, y1, y1), (x1, y2, y0), (x2, y1, y2)))
+    side = torch.cuda.Stream()
+
+    def step():
+        main = torch.cuda.current_stream()
+        first.run()
+        x1.copy_(y1)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            right.run()
+        left.run()
+        x2.copy_(y1)
+        main.wait_stream(side)
+        last.run()
+
+    side.wait_stream(torch.cuda.current_stream())
+    one = sf.lora_add(x, A, B, scale, ids, torch.empty_like(y1), y0)
+    b1 = one.to(torch.bfloat16)
+    two = sf.lora_add(b1, A, B, scale, ids, torch.empty_like(y1), one)
+    three = sf.lora_add(b1, A, B, scale, ids, torch.empty_like(y1), y0)
+    want = sf.lora_add(two.to(torch.bfloat16), A, B, scale, ids, torch.empty_like(y1), three)
+    for _ in range(3):
+        step()
+        torch.cuda.synchronize()
+        assert torch.equal(y1, want) and torch.equal(y2, three)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=torch.cuda.Stream()):
+        step()
+    for _ in range(3):
+        y1.zero_(), y2.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y1, want) and torch.equal(y2, three)
+
+
 # ---- a step of all of them -----------------------------------------------------------
 
 
