@@ -158,23 +158,32 @@ __device__ void lora_rows(const LoraArgs& P, Shared<KS>& S, const int* list, int
     const int r0 = p * C::RB;
     if (p > 0 && r0 >= a.rank) break;
     float acc[C::RB / 8][4] = {};
+    // A step's loads at once up to rank 32 (a decode batch's warp has one step: 8.6 us, 9.0 by halves); above, the
+    // registers do not allow it (rank 64: 23.4 us, 21.8 by halves).
+    constexpr int HALVES = KS <= 2 ? 2 : 1;
 #pragma unroll 1
-    for (int k = 64 * s0; k < 64 * s1; k += 32) {
-      const bool in = k + 8 * t < a.K;
-      uint4 xv[2], av[C::RB / 8];
+    for (int k = 64 * s0; k < 64 * s1; k += 32 * HALVES) {
+      uint4 xv[HALVES][2], av[HALVES][C::RB / 8];
 #pragma unroll
-      for (int j = 0; j < C::RB / 8; ++j)
-        av[j] = in && r0 + 8 * j < a.rank
-                    ? *reinterpret_cast<const uint4*>(Aw + static_cast<int64_t>(r0 + 8 * j) * a.K + k)
-                    : make_uint4(0, 0, 0, 0);
+      for (int h = 0; h < HALVES; ++h) {
+        const int at = k + 32 * h;
+        const bool in = at + 8 * t < a.K;
 #pragma unroll
-      for (int z = 0; z < 2; ++z)
-        xv[z] = in && r[z] < n ? *reinterpret_cast<const uint4*>(x[z] + k) : make_uint4(0, 0, 0, 0);
+        for (int j = 0; j < C::RB / 8; ++j)
+          av[h][j] = in && r0 + 8 * j < a.rank
+                         ? *reinterpret_cast<const uint4*>(Aw + static_cast<int64_t>(r0 + 8 * j) * a.K + at)
+                         : make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int j = 0; j < C::RB / 8; ++j) {
-        bmma(acc[j], xv[0].x, xv[1].x, xv[0].y, xv[1].y, av[j].x, av[j].y);
-        bmma(acc[j], xv[0].z, xv[1].z, xv[0].w, xv[1].w, av[j].z, av[j].w);
+        for (int z = 0; z < 2; ++z)
+          xv[h][z] = in && r[z] < n ? *reinterpret_cast<const uint4*>(x[z] + at) : make_uint4(0, 0, 0, 0);
       }
+#pragma unroll
+      for (int h = 0; h < HALVES; ++h)
+#pragma unroll
+        for (int j = 0; j < C::RB / 8; ++j) {
+          bmma(acc[j], xv[h][0].x, xv[h][1].x, xv[h][0].y, xv[h][1].y, av[h][j].x, av[h][j].y);
+          bmma(acc[j], xv[h][0].z, xv[h][1].z, xv[h][0].w, xv[h][1].w, av[h][j].z, av[h][j].w);
+        }
     }
     if (p > 0) __syncthreads();  // the sums of the pass before are read
 #pragma unroll
