@@ -882,11 +882,11 @@ sf_status sf_paged_append(const sf_paged_append_args* a, sf_stream_t stream);
  *           aligned, contents arbitrary, in use until the call's work ends.
  * Scores are exact integer products of the codes with q in 22-bit fixed point
  * relative to its row's largest entry; softmax weights enter the value product
- * as f16 pairs (22 bits); all sums are fp32.  For a bf16 output q is taken in 15
- * bits and the weights in 11, each well inside the output's own rounding for
- * keys of ordinary spread.  A row whose q holds a NaN or Inf gives NaN.  The
- * order of sums is fixed by the arguments' values, so equal calls give equal
- * bits.
+ * as f16 pairs (22 bits); all sums are fp32; a bf16 output is the fp32 one
+ * rounded once.  A row whose q holds a NaN or Inf gives NaN.  The order of sums
+ * is fixed by the sizes and the values of len and cu_rows, so equal calls give
+ * equal bits; a row beside other requests (or in a batch of other T or R) may
+ * differ in its last bits, since its cache is then split elsewhere.
  * Constraints: kv's; Hq a multiple of Hkv, Hq/Hkv <= 64, 1 <= R <= 8192,
  *   T >= 0, T * Hq/Hkv < 2^26, max_pages >= 1, max_pages * page_size < 2^31,
  *   window >= 0, scale finite; rows of q and out 16-byte aligned.

@@ -58,12 +58,11 @@ struct AttnArgs {
 //    score products' 16 columns are digit 0, digit 1 and twice digit 2 of the
 //    four, so a lane keeps one of its two tokens and half the softmax work, and
 //    the value product's columns are the four weights and their four remainders:
-//    half the products;
-//  * BF16, for bf16 outputs (which keep 8 bits): two digits of X = rint(q
-//    (1 - 2^-7) 2^(14-e)), |X| < 2^15 - 2^8 so that the digits do not run over,
-//    and the weights without their remainders (11 bits): close to half the
-//    products.  A score moves by some 2^-15 of a key's length times q's largest
-//    entry, a weight by 2^-12 of itself.
+//    half the products.
+// The output's type decides nothing but the last rounding.  (Two digits of q and
+// weights without remainders for bf16 outputs take 16% less time, 188 us for 223
+// with 64 requests of 1 to 4 rows, but lose bits of every channel below a
+// query's largest, and show in the bf16 output.)
 // The k index of the value product is free, so the tokens of a tile are
 // ordered such that both fragment loads are free of bank conflicts.
 //
@@ -74,18 +73,17 @@ struct AttnArgs {
 // log2(e)
 constexpr float kLog2e = 1.4426950408889634f;
 
-template <int D_, int NT_, bool PACK_, bool BF16_, int TOK_, int WARPS_, int STAGES_>
+template <int D_, int NT_, bool PACK_, int TOK_, int WARPS_, int STAGES_>
 struct Cfg {
   static constexpr int D = D_, NT = NT_, TOK = TOK_, WARPS = WARPS_, STAGES = STAGES_;
-  static constexpr bool PACK = PACK_, BF16 = BF16_;
-  static constexpr int DIGITS = BF16 ? 2 : 3;
-  static constexpr int FLUSH = BF16 ? 256 : 64 / TOK;  // a bf16 output does not notice
+  static constexpr bool PACK = PACK_;
+  static constexpr int FLUSH = 64 / TOK;  // stages
   static constexpr int COLS = PACK ? 4 : 8 * NT, GROUPS = TOK / 16;
   // tiles and tokens of a step of the inner loop: four tiles where the registers allow (128K tokens: 42 us; two, 45)
   static constexpr int TILES = NT == 1 && D <= 128 && WARPS == 8 ? 4 : 2, SUB = 16 * TILES;
   static_assert(TOK % SUB == 0, "whole steps");
   static constexpr bool SPLIT = NT == 1;  // odd codes as 16 c in sums of their own: fewer shifts, more sums
-  static constexpr int DT = PACK ? DIGITS - 1 : DIGITS;                      // products of 8 columns per k step and column tile
+  static constexpr int DT = PACK ? 2 : 3;                      // products of 8 columns per k step and column tile
   static constexpr int ROWS = PACK ? 1 : 2;                    // tokens of a tile whose scores a lane keeps
   static constexpr int KW = D / 32, VW = D / 64, MT = D / 16;  // words per lane of a K row, of a V row; dim tiles
   static constexpr int ROWB = D / 2, TILEB = 16 * ROWB, CH = D / 32;  // bytes of a row and of a tile; 16-byte chunks
@@ -542,22 +540,20 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) attn_paged_kernel(const __gr
           big = max(big >> 16, big & 0xFFFFu);
           const bool finite = big < 0x7F80u;
           const int e = finite ? max(static_cast<int>(big >> 7) - 127, -100) : 0;
-          constexpr int kExp = C::BF16 ? 14 : 21;
-          constexpr float kPart = C::BF16 ? 1.f - 0x1p-7f : 1.f;
-          const float up = __int_as_float((127 + kExp - e) << 23) * kPart;
+          constexpr int kExp = 21;
+          const float up = __int_as_float((127 + kExp - e) << 23);
           int sum = 0;
 #pragma unroll
           for (int j = 0; j < KW; ++j) {
             const uint32_t* p = reinterpret_cast<const uint32_t*>(&w[j]);
-            // X + 128 (1 + 256 + 65536) has the digits plus 128 in its bytes (without 65536 for two); X comes out of an
-            // fp32 sum's low bits
+            // X + 128 (1 + 256 + 65536) has the digits plus 128 in its bytes; X comes out of an fp32 sum's low bits
             uint32_t y[8];
 #pragma unroll
             for (int z = 0; z < 8; ++z) {  // dim 8 (KW t + j) + z
               const float v = __uint_as_float((z & 1) ? p[z >> 1] & 0xFFFF0000u : p[z >> 1] << 16);
               const uint32_t X = __float_as_uint(fmaf(v, up, 12582912.f)) - 0x4B400000u;  // (any, if not finite)
               sum += static_cast<int>(X);
-              constexpr uint32_t kBias = C::BF16 ? 0x8080u : 0x808080u;
+              constexpr uint32_t kBias = 0x808080u;
               y[z] = (X + kBias) ^ kBias;
             }
             uint32_t b[3][2];
@@ -573,17 +569,17 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) attn_paged_kernel(const __gr
             for (int z = 0; z < 2; ++z) {
               if constexpr (PACK) {
                 b_at(n, j, 0, z) = g < 4 ? b[0][z] : b[1][z];
-                if constexpr (C::DIGITS == 3) b_at(n, j, C::DT - 1, z) = b[2][z];
+                b_at(n, j, 1, z) = b[2][z];
               } else {
 #pragma unroll
-                for (int y = 0; y < C::DIGITS; ++y) b_at(n, j, y % C::DT, z) = b[y][z];
+                for (int y = 0; y < C::DT; ++y) b_at(n, j, y, z) = b[y][z];
               }
             }
           }
           sum += __shfl_xor_sync(0xffffffffu, sum, 1);
           sum += __shfl_xor_sync(0xffffffffu, sum, 2);
           // scores in base 2 from (16) sum X c
-          const float sc = finite ? __int_as_float((127 - (C::SPLIT ? 4 : 0) - kExp + e) << 23) * (A.scale * (kLog2e / kPart)) : NAN;
+          const float sc = finite ? __int_as_float((127 - (C::SPLIT ? 4 : 0) - kExp + e) << 23) * (A.scale * kLog2e) : NAN;
 #pragma unroll
           for (int z = 0; z < 2; ++z) {
             const int from = (col0 + z) * 4;
@@ -687,14 +683,12 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) attn_paged_kernel(const __gr
                 const int mine_a = digit(n, 0, z), mine_b = digit(n, 0, 2 + z);
                 const int other = __shfl_xor_sync(0xffffffffu, t < 2 ? mine_b : mine_a, 2);
                 f = fmaf(static_cast<float>(t < 2 ? mine_a : mine_b), own_w, static_cast<float>(other) * other_w);
-                if constexpr (C::DIGITS == 3)
-                  f = fmaf(static_cast<float>(t < 2 ? digit(n, C::DT - 1, z) : digit(n, C::DT - 1, 2 + z)), 65536.f, f);
+                f = fmaf(static_cast<float>(t < 2 ? digit(n, 1, z) : digit(n, 1, 2 + z)), 65536.f, f);
               } else {
-                f = C::SPLIT ? fmaf(static_cast<float>(digit(n, 1 % C::DT, 2 * k + z)), 256.f,
+                f = C::SPLIT ? fmaf(static_cast<float>(digit(n, 1, 2 * k + z)), 256.f,
                                     static_cast<float>(digit(n, 0, 2 * k + z)))
-                             : static_cast<float>(digit(n, 0, 2 * k + z) + 256 * digit(n, 1 % C::DT, 2 * k + z));
-                if constexpr (C::DIGITS == 3)
-                  f = fmaf(static_cast<float>(digit(n, C::DT - 1, 2 * k + z)), 65536.f, f);
+                             : static_cast<float>(digit(n, 0, 2 * k + z) + 256 * digit(n, 1, 2 * k + z));
+                f = fmaf(static_cast<float>(digit(n, C::DT - 1, 2 * k + z)), 65536.f, f);
               }
               s[j][n][k][z] = fmaf(-kz, qsum[n][z], f) * (ks * qsc[n][z]);
             }
@@ -791,7 +785,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) attn_paged_kernel(const __gr
       empty = false;
 
       // weights as operand fragments
-      constexpr int WT = PACK || C::BF16 ? 1 : 2;  // products of 8 columns per column tile
+      constexpr int WT = PACK ? 1 : 2;  // products of 8 columns per column tile
       uint32_t bw[TILES][NT][WT][2];
 #pragma unroll
       for (int j = 0; j < TILES; ++j)
@@ -810,17 +804,10 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) attn_paged_kernel(const __gr
             }
             const __half2 hh = __floats2half2_rn(w[0], w[1]);
             hi2[k] = reinterpret_cast<const uint32_t&>(hh);
-            if constexpr (!C::BF16) {
-              const float2 back = __half22float2(hh);
-              lo2[k] = h2_bits(w[0] - back.x, w[1] - back.y);
-            }
+            const float2 back = __half22float2(hh);
+            lo2[k] = h2_bits(w[0] - back.x, w[1] - back.y);
           }
-          if constexpr (PACK && C::BF16) {
-            // columns 0-3 the weights: lanes t and t ^ 2 hold the two tokens
-            const uint32_t y = __shfl_xor_sync(0xffffffffu, hi2[0], 2);
-            bw[j][n][0][0] = transpose8x8(t < 2 ? hi2[0] : 0u);
-            bw[j][n][0][1] = transpose8x8(t < 2 ? y : 0u);
-          } else if constexpr (PACK) {
+          if constexpr (PACK) {
             // columns 0-3 the weights, 4-7 the remainders: lanes t and t ^ 2 hold the two tokens of both
             const uint32_t y = __shfl_xor_sync(0xffffffffu, t < 2 ? lo2[0] : hi2[0], 2);
             bw[j][n][0][0] = transpose8x8(t < 2 ? hi2[0] : y);
@@ -829,7 +816,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) attn_paged_kernel(const __gr
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               bw[j][n][0][k] = transpose8x8(hi2[k]);
-              if constexpr (WT == 2) bw[j][n][WT - 1][k] = transpose8x8(lo2[k]);
+              bw[j][n][WT - 1][k] = transpose8x8(lo2[k]);
             }
           }
         }
@@ -902,7 +889,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) attn_paged_kernel(const __gr
             const float inv = l[n][z] == 0.f ? 0.f : 1.f / (l[n][z] * (vscale == 0.f ? 1.f : vscale));
 #pragma unroll
             for (int k = 0; k < MT; ++k) {
-              if constexpr (PACK && !C::BF16) {  // weights' and remainders' sums
+              if constexpr (PACK) {  // weights' and remainders' sums
                 acc[k][n][z] += __shfl_xor_sync(0xffffffffu, acc[k][n][z], 2);
                 acc[k][n][z + 2] += __shfl_xor_sync(0xffffffffu, acc[k][n][z + 2], 2);
               }
@@ -1089,21 +1076,21 @@ struct Kernel {
 // Calls f with the kernel for these sizes: 4 (packed), 8 or 16 columns a block, by the columns that a request's rows
 // fill on average (rounded down: a padded batch has a few rows more than its requests); d = 256 has no registers for
 // 16.
-template <bool BF16, class F>
+template <class F>
 auto with_kernel(int T, int R, int Hq, int Hkv, int d, F f) {
   const int64_t cols = static_cast<int64_t>(std::max(1, T / R)) * (Hq / Hkv);
   if (d == 64) {
-    if (cols <= 4) return f(Kernel<Cfg<64, 1, true, BF16, 64, 12, 3>>{});
-    if (cols <= 8) return f(Kernel<Cfg<64, 1, false, BF16, 64, 12, 3>>{});
-    return f(Kernel<Cfg<64, 2, false, BF16, 64, 8, 3>>{});
+    if (cols <= 4) return f(Kernel<Cfg<64, 1, true, 64, 12, 3>>{});
+    if (cols <= 8) return f(Kernel<Cfg<64, 1, false, 64, 12, 3>>{});
+    return f(Kernel<Cfg<64, 2, false, 64, 8, 3>>{});
   }
   if (d == 128) {
-    if (cols <= 4) return f(Kernel<Cfg<128, 1, true, BF16, 64, 8, 2>>{});
-    if (cols <= 8) return f(Kernel<Cfg<128, 1, false, BF16, 64, 8, 2>>{});
-    return f(Kernel<Cfg<128, 2, false, BF16, 64, 8, 2>>{});
+    if (cols <= 4) return f(Kernel<Cfg<128, 1, true, 64, 8, 2>>{});
+    if (cols <= 8) return f(Kernel<Cfg<128, 1, false, 64, 8, 2>>{});
+    return f(Kernel<Cfg<128, 2, false, 64, 8, 2>>{});
   }
-  if (cols <= 4) return f(Kernel<Cfg<256, 1, true, BF16, 32, 8, 2>>{});
-  return f(Kernel<Cfg<256, 1, false, BF16, 32, 8, 2>>{});
+  if (cols <= 4) return f(Kernel<Cfg<256, 1, true, 32, 8, 2>>{});
+  return f(Kernel<Cfg<256, 1, false, 32, 8, 2>>{});
 }
 
 }  // namespace
@@ -1117,7 +1104,7 @@ extern "C" sf_status sf_attn_paged_workspace_size(int T, int R, int Hq, int Hkv,
   SF_REQUIRE(T >= 0 && R >= 1 && R <= 8192, "%s: need T >= 0 and R in [1, 8192]", what);
   const int blocks = sf::sm_count();
   auto size = [&](auto k) { return k.bytes(blocks); };
-  *bytes = std::max(with_kernel<false>(T, R, Hq, Hkv, d, size), with_kernel<true>(T, R, Hq, Hkv, d, size));
+  *bytes = with_kernel(T, R, Hq, Hkv, d, size);
   return SF_OK;
 }
 
@@ -1173,6 +1160,5 @@ extern "C" sf_status sf_attn_paged(const sf_attn_paged_args* a, sf_stream_t stre
   A.window = a->window;
   A.bf16_out = a->out_type == SF_BF16;
   auto run = [&](auto k) { return k.launch(A, a->workspace, sf::sm_count(), sf::as_cuda(stream)); };
-  return a->out_type == SF_BF16 ? with_kernel<true>(a->T, a->R, a->Hq, kv.Hkv, kv.d, run)
-                                : with_kernel<false>(a->T, a->R, a->Hq, kv.Hkv, kv.d, run);
+  return with_kernel(a->T, a->R, a->Hq, kv.Hkv, kv.d, run);
 }
