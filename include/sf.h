@@ -804,7 +804,9 @@ typedef struct sf_paged_kv {
  *   cu_rows[R+1] exclusive sums of add;
  *   slots, positions, row_request [max_rows]: row r of request i is token
  *                position = keep + r - cu_rows[i], slot = page * page_size +
- *                position % page_size; rows behind the last: -1, 0, -1;
+ *                position % page_size (-1 where the table or the free list
+ *                holds a page outside [0, 2^31 / page_size)); rows behind the
+ *                last: -1, 0, -1;
  *   status[1]    SF_PLAN_OK, or why nothing was planned: SF_PLAN_LENGTH (len,
  *                keep or add negative, keep > len, or a length above max_pages
  *                * page_size), SF_PLAN_ROWS (more than max_rows rows),

@@ -6,7 +6,7 @@ S1  pages: a request's tokens lie in pages of P tokens, page j of request i is
 S2  plan: request i keeps keep_i of its len_i tokens and adds add_i.  The free
     list is a stack; first every page behind ceil((keep + add) / P) is pushed
     (requests in order, a request's pages in order), then the missing pages
-    are popped (same order).  Lengths out of range, more rows than there is
+    are popped (same order).  A page outside [0, 2^31 / P) gives slots of -1.  Lengths out of range, more rows than there is
     room for, or too few pages: nothing changes and the step has no rows.
 S3  a token-head's K or V row is quantized as one group with b = 4 (Q1-Q4 of
     the nested quantizer); its value is scale (code - zero).
@@ -57,7 +57,8 @@ def plan(lens, keep, add, table, free, free_cap: int, P: int, max_rows: int) -> 
     for i in range(R):
         cu.append(cu[-1] + add[i])
         for p in range(keep[i], keep[i] + add[i]):
-            slots.append(table[i][p // P] * P + p % P)
+            page = table[i][p // P]
+            slots.append(page * P + p % P if 0 <= page < 2 ** 31 // P else -1)
             positions.append(p)
             request.append(i)
     pad = max_rows - len(slots)

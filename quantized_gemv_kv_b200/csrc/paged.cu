@@ -2,6 +2,7 @@
 // append of its rows (sf_paged_append).
 #include <algorithm>
 #include <atomic>
+#include <climits>
 #include <cmath>
 
 #include <cooperative_groups.h>
@@ -188,7 +189,8 @@ __global__ void __launch_bounds__(512) paged_plan_kernel(const __grid_constant__
       pos[k] = kp[i] + (r0 + k - cu[i]);
       const int j = pos[k] >> shift;
       const int page = j < hv[i] ? a.block_table[i * a.table_stride + j] : a.free_list[top - (ct[i] + j - hv[i])];
-      slot[k] = page * a.page_size + (pos[k] & (a.page_size - 1));
+      // (a page whose slots would not fit 32 bits is in no pool, and must not come out as another page's)
+      if (page >= 0 && page <= INT_MAX >> shift) slot[k] = (page << shift) + (pos[k] & (a.page_size - 1));
     }
     if (P.vec && own == 4 && r0 + 4 <= a.max_rows) {
       *reinterpret_cast<int4*>(a.slots + r0) = make_int4(slot[0], slot[1], slot[2], slot[3]);

@@ -1,0 +1,48 @@
+"""The serving operators at the ends of their ranges: page numbers that no pool
+has, plans made by several host threads, rotations bit by bit, token-heads of
+every size, long inner loops of the adapters, values near the largest float."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import serving as osv
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def sf():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    import quantized_gemv_kv_b200 as sf
+    return sf
+
+
+def _dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def _i32(a):
+    return _dev(np.asarray(a, dtype=np.int32))
+
+
+# ---- plan ------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("P", [16, 64, 256])
+def test_plan_page_numbers_that_no_pool_has(sf, P):
+    """A table or free-list entry whose tokens' slots would not fit 32 bits gives slots of -1, never another page's."""
+    first = 2 ** 31 // P                                  # (2^31 / P) P + 16 would come out as slot 16
+    bad = [first, first + 1, 2 ** 31 - 1, -(2 ** 31), -1, -first]
+    table = np.array([[b, first - 1] for b in bad])
+    lens, add = [P // 2] * len(bad), [P // 2 + 2] * len(bad)    # rows on the first page and, from the list, the second
+    free = bad[::-1]
+    want = osv.plan(lens, lens, add, table.tolist(), free, 8, P, 2048)
+    job = sf.paged_plan(_i32(lens), _i32(add), _i32(table), _i32(free + [0, 0]), _i32([len(free)]), P, 2048)
+    assert int(job.status.item()) == osv.PLAN_OK
+    assert job.slots.tolist() == want["slots"] == [-1] * 2048
+    assert job.positions.tolist() == want["positions"] and job.row_request.tolist() == want["request"]
+    # the last page that there can be
+    last = sf.paged_plan(_i32([P - 1]), _i32([1]), _i32([[first - 1]]), _i32([0]), _i32([0]), P, 1)
+    assert last.slots.tolist() == [2 ** 31 - 1]
