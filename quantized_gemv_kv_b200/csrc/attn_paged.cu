@@ -1057,15 +1057,10 @@ struct Kernel {
     W.parts = reinterpret_cast<float*>(static_cast<char*>(ws) + tails_bytes(blocks));
     W.heads = W.parts + static_cast<size_t>(blocks) * 2 * C::PART;
     W.blocks = blocks;
-    static std::atomic<unsigned long long> allowed{0};  // devices that have been told of the kernel's shared memory
-    int dev = 0;
-    SF_CHECK_CUDA(cudaGetDevice(&dev));
-    const unsigned long long bit = 1ull << (dev & 63);
-    if ((allowed.load(std::memory_order_relaxed) & bit) == 0) {
-      SF_CHECK_CUDA(cudaFuncSetAttribute(attn_paged_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
-      if (dev < 64) allowed.fetch_or(bit, std::memory_order_relaxed);
-    }
-    sf_status st = sf::launch("attn_paged_kernel", attn_paged_kernel<C>, dim3(blocks), 32 * C::WARPS, C::SMEM, 1, s, W);
+    static std::atomic<unsigned long long> told{0};
+    sf_status st = sf::allow_smem(attn_paged_kernel<C>, C::SMEM, told);
+    if (st != SF_OK) return st;
+    st = sf::launch("attn_paged_kernel", attn_paged_kernel<C>, dim3(blocks), 32 * C::WARPS, C::SMEM, 1, s, W);
     if (st != SF_OK) return st;
     // its blocks start as the first kernel's end, and wait for the last
     return sf::launch("attn_paged_join_kernel", attn_paged_join_kernel<C>, dim3(blocks), 32 * C::COLS * C::JOIN, 0, 1,

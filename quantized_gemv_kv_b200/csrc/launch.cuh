@@ -5,6 +5,8 @@
 // kernels that follow one another).
 #pragma once
 
+#include <atomic>
+
 #include "sf_internal.h"
 
 namespace sfd {
@@ -17,6 +19,21 @@ __device__ __forceinline__ void let_next_prepare() { asm volatile("griddepcontro
 }  // namespace sfd
 
 namespace sf {
+
+// Lets a kernel have `bytes` of dynamic shared memory (and, where `wide`, clusters of sixteen blocks): told once per
+// device.  A kernel's limit is one for the whole process, so the number must not depend on the call: another thread's
+// could come between this one and the launch.  told: one variable per kernel, of devices that know.
+template <class P>
+sf_status allow_smem(void (*kernel)(P), size_t bytes, std::atomic<unsigned long long>& told, bool wide = false) {
+  int dev = 0;
+  SF_CHECK_CUDA(cudaGetDevice(&dev));
+  const unsigned long long bit = 1ull << (dev & 63);
+  if ((told.load(std::memory_order_relaxed) & bit) != 0) return SF_OK;
+  SF_CHECK_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)));
+  if (wide) SF_CHECK_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
+  if (dev < 64) told.fetch_or(bit, std::memory_order_relaxed);
+  return SF_OK;
+}
 
 // cluster: blocks per thread-block cluster (1: none).
 template <class P>

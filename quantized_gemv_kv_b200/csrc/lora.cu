@@ -372,9 +372,9 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const __grid_constant
 template <int KS>
 sf_status launch_lora(const LoraArgs& P, int clusters, cudaStream_t s) {
   const size_t smem = sizeof(Shared<KS>);
-  if (smem > 48 * 1024)
-    SF_CHECK_CUDA(
-        cudaFuncSetAttribute(lora_kernel<KS>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
+  static std::atomic<unsigned long long> told{0};
+  const sf_status st = sf::allow_smem(lora_kernel<KS>, smem, told);
+  if (st != SF_OK) return st;
   return sf::launch("lora_kernel", lora_kernel<KS>, dim3(clusters << P.log_blocks), kThreads, smem, 1 << P.log_blocks, s,
                     P);
 }

@@ -528,13 +528,11 @@ extern "C" sf_status sf_paged_plan(const sf_paged_plan_args* a, sf_stream_t stre
   // that has many (1000 requests, 65536 rows: 10 us; 13 with eight of 1024 threads).
   const bool small = a->R <= 128 && a->max_rows <= 512;
   const int blocks = small || a->max_rows <= 4096 ? 1 : 16;
-  const size_t smem = static_cast<size_t>(kPlanArrays) * (a->R + 1) * sizeof(int);
-  if (smem > 48 * 1024)
-    SF_CHECK_CUDA(cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem)));
-  if (blocks > 8)
-    SF_CHECK_CUDA(cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
-  return sf::launch("paged_plan_kernel", paged_plan_kernel, dim3(blocks), small ? 128 : 512, smem, blocks,
+  auto smem_for = [](int R) { return static_cast<size_t>(kPlanArrays) * (R + 1) * sizeof(int); };
+  static std::atomic<unsigned long long> told{0};
+  const sf_status st = sf::allow_smem(paged_plan_kernel, smem_for(kPlanMaxR), told, true);
+  if (st != SF_OK) return st;
+  return sf::launch("paged_plan_kernel", paged_plan_kernel, dim3(blocks), small ? 128 : 512, smem_for(a->R), blocks,
                     sf::as_cuda(stream), P);
 }
 

@@ -2,6 +2,8 @@
 has, plans made by several host threads, rotations bit by bit, token-heads of
 every size, long inner loops of the adapters, values near the largest float."""
 
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -46,3 +48,27 @@ def test_plan_page_numbers_that_no_pool_has(sf, P):
     # the last page that there can be
     last = sf.paged_plan(_i32([P - 1]), _i32([1]), _i32([[first - 1]]), _i32([0]), _i32([0]), P, 1)
     assert last.slots.tolist() == [2 ** 31 - 1]
+
+
+def test_plans_of_several_host_threads(sf):
+    """Plans of different sizes made at once: each call's shared memory is its own."""
+    P, errors = 16, []
+
+    def loop(R):
+        try:
+            lens = _i32([0] * R)
+            with torch.cuda.stream(torch.cuda.Stream()):
+                job = sf.PagedPlan(lens, _i32([1] * R), _i32(np.full((R, 2), -1)), _i32(np.arange(R)), _i32([R]), P, R,
+                                   lens_out=torch.empty_like(lens), n_free_out=_i32([0]))
+                for _ in range(3000):
+                    job.run()
+        except Exception as e:  # noqa: BLE001 - handed to the test
+            errors.append(e)
+
+    threads = [threading.Thread(target=loop, args=(R,)) for R in (2600, 8192, 4000, 6000)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors, errors[0]
