@@ -546,10 +546,10 @@ extern "C" sf_status sf_paged_append(const sf_paged_append_args* a, sf_stream_t 
   SF_REQUIRE(a->src_type == SF_F32 || a->src_type == SF_BF16, "%s: src_type must be SF_F32 or SF_BF16", what);
   SF_REQUIRE(a->Hq >= 0 && a->Hq <= 1024, "%s: Hq must be in [0, 1024]", what);
   SF_REQUIRE(a->theta >= 0.0 && std::isfinite(a->theta), "%s: theta must be finite and >= 0", what);
+  SF_REQUIRE(a->theta > 0.0 || a->Hq == 0, "%s: q is only rotated: it needs theta > 0", what);
+  if (a->T == 0) return SF_OK;  // (tensors without elements have no address)
   SF_REQUIRE((a->q != nullptr) == (a->Hq > 0) && (a->q_out != nullptr) == (a->Hq > 0),
              "%s: q and q_out go with Hq > 0", what);
-  SF_REQUIRE(a->theta > 0.0 || a->Hq == 0, "%s: q is only rotated: it needs theta > 0", what);
-  if (a->T == 0) return SF_OK;
   SF_REQUIRE(a->k && a->v && a->slots, "%s: null pointer", what);
   SF_REQUIRE(a->theta == 0.0 || a->positions, "%s: the rotation needs positions", what);
   const int es = a->src_type == SF_F32 ? 4 : 2;

@@ -72,3 +72,21 @@ def test_plans_of_several_host_threads(sf):
         t.join()
     torch.cuda.synchronize()
     assert not errors, errors[0]
+
+
+# ---- append ----------------------------------------------------------------------
+
+
+def test_calls_without_rows(sf):
+    """T = 0, an append with queries and without, attention, adapters: nothing to do."""
+    kv = sf.PagedKV.empty(2, 2, 16, 64)
+    k = torch.zeros((0, 2, 64), device="cuda")
+    q = torch.zeros((0, 4, 64), device="cuda")
+    none = _i32(np.zeros(0))
+    assert sf.paged_append(kv, k, k, none) is None
+    out = sf.paged_append(kv, k, k, none, none, 10000.0, q)
+    assert out.shape == (0, 4, 64) and torch.all(kv.k_param == 0)
+    got = sf.attn_paged(out, kv, _i32([0, 0]), _i32([0]), _i32([[0]]))
+    assert got.shape == (0, 4, 64)
+    x, A, B = (torch.zeros(s, dtype=torch.bfloat16, device="cuda") for s in ((0, 16), (1, 8, 16), (1, 5, 8)))
+    assert sf.lora_add(x, A, B, torch.ones(1, device="cuda"), none).shape == (0, 5)
