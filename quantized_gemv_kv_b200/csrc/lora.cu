@@ -212,7 +212,8 @@ __device__ void lora_rows(const LoraArgs& P, Shared<KS>& S, const int* list, int
     sum *= scale;
 #pragma unroll
     for (int z = 0; z < 3; ++z) {
-      const __nv_bfloat16 t16 = __float2bfloat16_rn(sum);
+      __nv_bfloat16 t16 = __float2bfloat16_rn(sum);
+      if (z == 0 && __hisinf(t16) && !isinf(sum)) t16 = __float2bfloat16_rz(sum);  // above bf16's largest: cut
       S.term[z][e / C::RK][e % C::RK] = __bfloat16_as_ushort(t16);
       sum = isinf(sum) ? 0.f : sum - __bfloat162float(t16);  // an infinity has no remainder
     }

@@ -90,3 +90,22 @@ def test_calls_without_rows(sf):
     assert got.shape == (0, 4, 64)
     x, A, B = (torch.zeros(s, dtype=torch.bfloat16, device="cuda") for s in ((0, 16), (1, 8, 16), (1, 5, 8)))
     assert sf.lora_add(x, A, B, torch.ones(1, device="cuda"), none).shape == (0, 5)
+
+
+# ---- adapters --------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("rank", [8, 24, 128])
+def test_lora_near_the_largest_float(sf, rank):
+    """scale A x between the largest bf16 and the largest fp32 value: finite outputs stay finite."""
+    K, N = 64, 40
+    x = torch.zeros((2, K), dtype=torch.bfloat16)
+    A = torch.zeros((1, rank, K), dtype=torch.bfloat16)
+    B = torch.zeros((1, N, rank), dtype=torch.bfloat16)
+    x[:, 3] = torch.tensor([1.0, -1.0])
+    A[0, 5, 3] = 2.0 ** 127
+    B[0, :, 5] = torch.linspace(-0.5, 0.5, N).to(torch.bfloat16)
+    scale = torch.tensor([1.9999])
+    out = sf.lora_add(x.cuda(), A.cuda(), B.cuda(), scale.cuda(), _i32([0, 0]), y=torch.zeros((2, N), device="cuda"))
+    want = x[:, 3:4].double() * scale.double() * 2.0 ** 127 * B[0, :, 5].double()
+    assert torch.all((out.cpu().double() - want).abs() <= 2.0 ** -22 * want.abs())
