@@ -24,7 +24,6 @@ SF_F32, SF_BF16 = 0, 1
 PLAN_OK, PLAN_LENGTH, PLAN_ROWS, PLAN_PAGES = range(4)
 _DTYPES = {torch.float32: SF_F32, torch.bfloat16: SF_BF16}
 _i64 = ctypes.c_int64
-_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
 class _PagedKV(ctypes.Structure):
@@ -127,12 +126,12 @@ class _Job:
         stream that was current then: order ``stream`` behind it, and keep
         the object until the call's work has ended."""
         if stream is None:
-            raw = _raw_stream(self._index)  # torch.cuda.current_stream().cuda_stream, without the Stream object
+            raw = torch._C._cuda_getCurrentRawStream(self._index)  # the current stream, without a Stream object
         elif stream.device != self.device:
             raise ValueError(f"stream is on {stream.device}, the tensors on {self.device}")
         else:
             raw = stream.cuda_stream
-        if _current_device() == self._index:
+        if torch._C._cuda_getDevice() == self._index:
             status = self._call(self._ref, raw)
         else:
             with torch.cuda.device(self.device):

@@ -3,8 +3,13 @@ import on a PyTorch without the CUDA bindings, workspaces sized for the tensors'
 own device."""
 
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module")
@@ -23,3 +28,14 @@ def test_append_without_rows_needs_no_pointers(sf):
         assert sf._lib.sf_paged_append(ctypes.byref(args), None) == sf.SF_OK
     args = _AppendArgs(ctypes.pointer(kv), None, None, None, None, None, None, None, None, 256, 256, 512, 512, 0.0, 0, 4, 0)
     assert sf._lib.sf_paged_append(ctypes.byref(args), None) == sf.SF_EINVAL   # queries without a rotation all the same
+
+
+def test_import_without_torch_cuda_bindings():
+    """A PyTorch built without CUDA lacks the raw bindings: the package imports, and only calls need them."""
+    code = ("import torch\n"
+            "for n in ('_cuda_getCurrentRawStream', '_cuda_getDevice'):\n"
+            "    if hasattr(torch._C, n): delattr(torch._C, n)\n"
+            "import quantized_gemv_kv_b200 as sf\n"
+            "assert sf.attn_paged_workspace_size(3, 2, 4, 2, 128) > 0\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
