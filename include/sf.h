@@ -880,8 +880,10 @@ sf_status sf_paged_append(const sf_paged_append_args* a, sf_stream_t stream);
  *   block_table int32 [R][table_stride], max_pages entries per request; tokens
  *           in pages outside [0, num_pages) are left out.
  *   cu_rows int32 [R + 1], ascending; rows at or behind T are left out.
- *   workspace device scratch of sf_attn_paged_workspace_size bytes, 16-byte
- *           aligned, contents arbitrary, in use until the call's work ends.
+ *   workspace device scratch of sf_attn_paged_workspace_size bytes (asked
+ *           with the same device current: it goes by the number of SMs),
+ *           16-byte aligned, contents arbitrary, in use until the call's work
+ *           ends.
  * Scores are exact integer products of the codes with q in 22-bit fixed point
  * relative to its row's largest entry; softmax weights enter the value product
  * as f16 pairs (22 bits); all sums are fp32; a bf16 output is the fp32 one

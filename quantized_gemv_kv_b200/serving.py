@@ -314,9 +314,12 @@ def paged_append(kv, k, v, slots, positions=None, theta=0.0, q=None, q_out=None,
 # ---- sf_attn_paged ----------------------------------------------------------------
 
 
-def attn_paged_workspace_size(T: int, R: int, Hq: int, Hkv: int, d: int) -> int:
+def attn_paged_workspace_size(T: int, R: int, Hq: int, Hkv: int, d: int, device=None) -> int:
+    """Bytes of workspace that ``attn_paged`` needs on ``device`` (default:
+    the current one); it goes by the device's number of SMs."""
     out = _sz()
-    _check(_lib.sf_attn_paged_workspace_size(T, R, Hq, Hkv, d, ctypes.byref(out)))
+    with contextlib.nullcontext() if device is None else torch.cuda.device(device):
+        _check(_lib.sf_attn_paged_workspace_size(T, R, Hq, Hkv, d, ctypes.byref(out)))
     return out.value
 
 
@@ -347,14 +350,13 @@ class PagedAttention(_Job):
         if out is None:
             out = torch.zeros((T, Hq, d), dtype=torch.float32, device=q.device)
         os_ = _matrix("out", out, tuple(_DTYPES), (T, Hq, d))
-        need = attn_paged_workspace_size(T, R, Hq, kv.Hkv, d)
+        dev = _same_device("q", q=q, k_codes=kv.k_codes, cu_rows=cu_rows, lens=lens, block_table=block_table,
+                           out=out, workspace=workspace)
+        need = attn_paged_workspace_size(T, R, Hq, kv.Hkv, d, device=dev)
         if workspace is None:
-            _dev(q, "q")
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
-        dev = _same_device("q", q=q, k_codes=kv.k_codes, cu_rows=cu_rows, lens=lens, block_table=block_table,
-                           out=out, workspace=workspace)
         self.out, self.workspace = out, workspace
         a = _AttnArgs(ctypes.pointer(kv._c), q.data_ptr(), cu_rows.data_ptr(), lens.data_ptr(),
                       block_table.data_ptr(), out.data_ptr(), workspace.data_ptr(),

@@ -2,12 +2,14 @@
 import on a PyTorch without the CUDA bindings, workspaces sized for the tensors'
 own device."""
 
+import contextlib
 import ctypes
 import os
 import subprocess
 import sys
 
 import pytest
+import torch
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -39,3 +41,40 @@ def test_import_without_torch_cuda_bindings():
             "assert sf.attn_paged_workspace_size(3, 2, 4, 2, 128) > 0\n")
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr
+
+
+def test_workspace_is_sized_on_the_tensors_device(sf, monkeypatch):
+    """The workspace goes by the number of SMs of the device that the call runs on, not of the current one."""
+    from quantized_gemv_kv_b200 import serving
+    at = [torch.device("cuda", 0)]
+    asked = []
+
+    @contextlib.contextmanager
+    def device(d):
+        at.append(torch.device(d))
+        yield
+        at.pop()
+
+    def size(T, R, Hq, Hkv, d, out):
+        asked.append(at[-1])
+        ctypes.cast(out, ctypes.POINTER(ctypes.c_size_t))[0] = 4096
+        return 0
+
+    class Lib:
+        sf_attn_paged_workspace_size = staticmethod(size)
+
+    monkeypatch.setattr(serving, "_lib", Lib)
+    monkeypatch.setattr(serving, "_dev", lambda t, name: None)
+    monkeypatch.setattr(serving, "_same_device", lambda first, **t: torch.device("cuda", 1))
+    monkeypatch.setattr(torch.cuda, "device", device)
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    param = torch.zeros((4, 2, 16, 2), dtype=torch.float16)
+    kv = serving.PagedKV(i32(4, 2, 16, 16), param, i32(4, 2, 16, 16), param)
+    q = torch.zeros((3, 4, 128), dtype=torch.bfloat16)
+    job = serving.PagedAttention(q, kv, i32(3), i32(2), i32(2, 4))
+    assert job.workspace.numel() == 4096 and job.device == torch.device("cuda", 1)
+    assert asked and all(d == torch.device("cuda", 1) for d in asked)
+    asked.clear()
+    assert serving.attn_paged_workspace_size(3, 2, 4, 2, 128, device="cuda:1") == 4096
+    assert serving.attn_paged_workspace_size(3, 2, 4, 2, 128) == 4096
+    assert asked == [torch.device("cuda", 1), torch.device("cuda", 0)]
