@@ -29,6 +29,16 @@ def _i32(a):
     return _dev(np.asarray(a, dtype=np.int32))
 
 
+def _f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def _to_bf16(a):
+    """fp64 rounded once to bf16 (ties to even, subnormals of steps 2^-133), as fp64."""
+    step = np.maximum(np.frexp(a)[1] - 8, -133)
+    return np.ldexp(np.rint(np.ldexp(a, -step)), step)
+
+
 # ---- plan ------------------------------------------------------------------------
 
 
@@ -48,6 +58,21 @@ def test_plan_page_numbers_that_no_pool_has(sf, P):
     # the last page that there can be
     last = sf.paged_plan(_i32([P - 1]), _i32([1]), _i32([[first - 1]]), _i32([0]), _i32([0]), P, 1)
     assert last.slots.tolist() == [2 ** 31 - 1]
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_plan_negative_free_count(sf, in_place):
+    """Refused on the device like any other plan: every output as it has to be, inputs as they were."""
+    lens, add, table, free, rows = [40, 20, 0], [1, 1, 1], [[3, 5, 1, -1], [0, 2, -1, -1], [-1] * 4], [4, 6, 7], 8
+    d_lens, d_n, tab, lst = _i32(lens), _i32([-1]), _i32(table), _i32(free)
+    kw = {} if in_place else dict(lens_out=torch.full_like(d_lens, -9), n_free_out=torch.full_like(d_n, -9))
+    job = sf.paged_plan(d_lens, _i32(add), tab, lst, d_n, 16, rows, **kw)
+    assert int(job.status.item()) == osv.PLAN_PAGES
+    assert job.lens_out.tolist() == lens and d_lens.tolist() == lens
+    assert job.n_free_out.tolist() == [-1] and d_n.tolist() == [-1]
+    assert tab.tolist() == table and lst.tolist() == free and job.cu_rows.tolist() == [0] * 4
+    assert job.slots.tolist() == [-1] * rows and job.positions.tolist() == [0] * rows
+    assert job.row_request.tolist() == [-1] * rows
 
 
 def test_plans_of_several_host_threads(sf):
@@ -92,7 +117,101 @@ def test_calls_without_rows(sf):
     assert sf.lora_add(x, A, B, torch.ones(1, device="cuda"), none).shape == (0, 5)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("src", ["fp32", "bf16"])
+@pytest.mark.parametrize("gain", [1.0, 1e-36, 1e30])
+def test_append_rotates_queries_to_the_bit(sf, d, src, gain):
+    """q_out is the fp64 rotation rounded once to bf16.  An angle is off by its own rounding (positions below 2^20: 2^-33,
+    twice for two implementations), an entry by 2^-31 of its pair's size at most: between the two ends' roundings."""
+    T, Hq, theta = 700, 8, 500000.0
+    g = torch.Generator().manual_seed(d)
+    q = (torch.randn((T, Hq, d), generator=g) * gain).to(torch.float32 if src == "fp32" else torch.bfloat16)
+    pos = np.random.default_rng(d).integers(0, 1 << 20, T).astype(np.int32)
+    pos[:3] = 0, 1, 2 ** 20 - 1
+    kv = sf.PagedKV.empty(-(-T // 16), 1, 16, d)
+    k = torch.zeros((T, 1, d), dtype=q.dtype, device="cuda")
+    got = sf.paged_append(kv, k, k, _i32(np.arange(T)), _i32(pos), theta, q.cuda())
+    x, got = _f64(q), _f64(got)
+    want = osv.rope_rows(x, pos, theta)
+    size = np.abs(x[..., :d // 2]) + np.abs(x[..., d // 2:])
+    e = 2.0 ** -31 * np.concatenate([size, size], -1)
+    lo, hi = _to_bf16(want - e), _to_bf16(want + e)
+    assert np.mean(lo != hi) < 1e-5
+    assert np.all((got >= lo) & (got <= hi))
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_append_quantizes_every_size(sf, d):
+    """Token-heads from 2^-40 to 2^40, offset to either side, constant ones, one entry apart, spans that overflow: codes,
+    scales and zero points are the quantizer's."""
+    rng = np.random.default_rng(d)
+    rows = []
+    for e in range(-40, 41, 2):
+        z = rng.standard_normal((5, d))
+        z[1] += 30.0
+        z[2] -= 30.0
+        z[3] = 1.0
+        z[4] = 0.0
+        z[4, 5] = 1.0
+        rows.append(z * 2.0 ** e)
+    rows.append(np.where(np.arange(d) % 2, 3e38, -3e38)[None])
+    rows.append(np.full((1, d), -1e-42))
+    x = np.concatenate(rows).astype(np.float32)
+    T = len(x)
+    kv = sf.PagedKV.empty(-(-T // 16), 1, 16, d)
+    xd = _dev(x[:, None])
+    sf.paged_append(kv, xd, xd, _i32(np.arange(T)))
+    with np.errstate(over="ignore"):
+        c, s, z = osv.quantize_rows(x)
+    for codes, param in ((kv.k_codes, kv.k_param), (kv.v_codes, kv.v_param)):
+        w = codes.reshape(-1, d // 8)[:T].cpu().numpy().view(np.uint32)
+        got = ((w[..., None] >> (4 * np.arange(8, dtype=np.uint32))) & 15).reshape(T, d)
+        p = param.reshape(-1, 2)[:T].cpu().numpy()
+        np.testing.assert_array_equal(p[:, 0], s)
+        np.testing.assert_array_equal(p[:, 1], z)
+        np.testing.assert_array_equal(got, c)
+
+
 # ---- adapters --------------------------------------------------------------------
+
+
+def _lora(T, K, N, rank, n, seed, positive=False):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x, A, B = (torch.randn(s, generator=g, device="cuda") for s in ((T, K), (n, rank, K), (n, N, rank)))
+    if positive:
+        x, A = x.abs(), A.abs()
+    return (x.to(torch.bfloat16), (A / K ** 0.5).to(torch.bfloat16), B.to(torch.bfloat16),
+            torch.rand(n, generator=g, device="cuda") + 0.5, torch.randn((T, N), generator=g, device="cuda"))
+
+
+def _lora_exact(x, A, B, scale, ids, y):
+    """The formula in 64 bits, and the same of absolute values."""
+    out, size = y.double(), torch.zeros(y.shape, dtype=torch.float64, device="cuda")
+    for a in range(len(A)):
+        rows = (ids == a).nonzero()[:, 0]
+        for at, f in ((out, lambda t: t.double()), (size, lambda t: t.double().abs())):
+            at[rows] += f(scale[a]) * ((f(x[rows]) @ f(A[a]).t()) @ f(B[a]).t())
+    return out, size
+
+
+@pytest.mark.parametrize("positive", [False, True])
+@pytest.mark.parametrize("T,K,N,rank,n,runs", [
+    # several steps of a warp's part of K
+    (3, 12288, 200, 16, 2, 1), (9, 12296, 96, 32, 3, 1), (20, 16384, 40, 64, 4, 1), (2, 14336, 64, 128, 1, 1),
+    # so many rows that a cluster has two blocks, and one
+    (2400, 2048, 96, 32, 4, 100), (2401, 2056, 36, 72, 3, 7), (4801, 12288, 40, 16, 5, 300), (4777, 2048, 64, 64, 3, 1),
+    (4900, 2048, 40, 128, 4, 50)])
+def test_lora_long_loops_and_small_clusters(sf, T, K, N, rank, n, runs, positive):
+    """A sum over K runs through at most K/16 tensor-core products (truncated: 2^-23 of the sum each) and 72 partial sums,
+    the second product through 3 rank/16 and the output's own: 2^-24 (|out| + (K/8 + rank/2 + 80) M), M the formula of
+    absolute values."""
+    x, A, B, scale, y = _lora(T, K, N, rank, n, T + K, positive)
+    ids = _i32(np.repeat(np.random.default_rng(T).integers(-1, n, T), runs)[:T])
+    out = sf.lora_add(x, A, B, scale, ids, torch.full((T, N), 7.0, device="cuda"), y)
+    want, size = _lora_exact(x, A, B, scale, ids, y)
+    err = (out.double() - want).abs()
+    print("error over the formula of absolute values", (err / (size + want.abs()).clamp(min=1e-30)).max().item())
+    assert torch.all(err <= 2.0 ** -24 * (want.abs() + (K / 8 + rank / 2 + 80) * size))
 
 
 @pytest.mark.parametrize("rank", [8, 24, 128])

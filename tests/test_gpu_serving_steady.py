@@ -143,6 +143,36 @@ KERNELS = [(64, 16, 4, 64, 1), (64, 24, 4, 16, 1), (64, 40, 4, 256, 1), (64, 12,
 
 
 @pytest.mark.parametrize("d,Hq,Hkv,P,rows", KERNELS)
+def test_several_stages_a_warp(sf, d, Hq, Hkv, P, rows):
+    rng = np.random.default_rng(d + Hq + rows)
+    lens = _mixed(rng, [30011, 60000, 8200, 14021], 9)
+    n = [int(min(x, rng.integers(1, rows + 1))) for x in lens]
+    c = Cache(sf, 3, n, lens, Hq, Hkv, d, P)
+    cols = 16 if Hq // Hkv * rows > 8 and d < 256 else 8 if Hq // Hkv * rows > 4 else 4
+    tok, warps = (32, 8) if d == 256 else (64, 12 if d == 64 and cols < 16 else 8)
+    units = sum(-(-k * (Hq // Hkv) // cols) * Hkv * -(-x // tok) for k, x in zip(n, lens))
+    assert units >= 3 * warps * torch.cuda.get_device_properties(0).multi_processor_count
+    want, tol = c.exact()
+    out = c.run(sf, torch.float32)
+    live = int(c.cu[-1])
+    err = (out.double() - want).abs()
+    print("largest error", err[:live].max().item(), "of its tolerance", (err / tol)[:live].nan_to_num().max().item(),
+          "tolerance over the largest value", (tol[:live].max() / want[:live].abs().max()).item())
+    assert torch.all(err <= tol)
+    assert torch.all(out[live:] == 7.0)
+
+
+@pytest.mark.parametrize("d,Hq,Hkv,P,rows", [KERNELS[0], KERNELS[6], KERNELS[7], KERNELS[9]])
+def test_several_stages_a_warp_with_a_window(sf, d, Hq, Hkv, P, rows):
+    rng = np.random.default_rng(d + Hq + rows + 1)
+    lens = _mixed(rng, [30011, 9000, 40000], 7)
+    c = Cache(sf, 4, [int(min(x, rng.integers(1, rows + 1))) for x in lens], lens, Hq, Hkv, d, P)
+    want, tol = c.exact(window=5003)
+    out = c.run(sf, torch.float32, window=5003)
+    assert torch.all((out.double() - want).abs() <= tol)
+
+
+@pytest.mark.parametrize("d,Hq,Hkv,P,rows", KERNELS)
 def test_bf16_outputs_are_the_fp32_ones_rounded(sf, d, Hq, Hkv, P, rows):
     """Nothing but the last rounding depends on the output's type: long caches, and queries and keys whose largest
     channels are some hundred times the others."""
