@@ -990,8 +990,8 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) attn_paged_kernel(const __gr
   }
 }
 
-// Joins the parts of the segment that starts in block b and ends in a later one: SPLIT warps per column, each taking
-// every SPLIT-th part, so that all their loads are on their way at once.
+// Joins the parts of the segment that starts in block b and ends in a later one: JOIN warps per column, each taking
+// every JOIN-th part, so that all their loads are on their way at once.
 template <class C>
 __global__ void __launch_bounds__(32 * C::COLS * C::JOIN) attn_paged_join_kernel(const __grid_constant__ Work W) {
   constexpr int D = C::D, Z = (D + 127) / 128;

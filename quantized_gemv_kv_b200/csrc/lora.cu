@@ -154,9 +154,8 @@ __device__ void lora_rows(const LoraArgs& P, Shared<KS>& S, const int* list, int
   const int s1 = static_cast<int>(static_cast<uint64_t>(steps) * (w + 1) >> (P.log_blocks + 3));
   const uint16_t* const Aw = a.A + (static_cast<int64_t>(id) * a.rank + g) * a.K + 8 * t;
 #pragma unroll
-  for (int p = 0; p < C::RK / C::RB; ++p) {
+  for (int p = 0; p < C::RK / C::RB; ++p) {  // (two passes only for ranks above 64)
     const int r0 = p * C::RB;
-    if (p > 0 && r0 >= a.rank) break;
     float acc[C::RB / 8][4] = {};
     // A step's loads at once up to rank 32 (a decode batch's warp has one step: 8.6 us, 9.0 by halves); above, the
     // registers do not allow it (rank 64: 23.4 us, 21.8 by halves).
@@ -199,8 +198,6 @@ __device__ void lora_rows(const LoraArgs& P, Shared<KS>& S, const int* list, int
       for (int v = 0; v < kWarps; ++v) sum += S.part[v][row][c];
       S.h[row * C::RK + r0 + c] = r0 + c < a.rank ? sum : 0.f;  // (an infinite x times the zeros behind the rank)
     }
-    if (p + 1 < C::RK / C::RB && r0 + C::RB >= a.rank)  // ranks of the next pass that there are not
-      for (int e = tid; e < kRows * C::RB; e += kThreads) S.h[e / C::RB * C::RK + r0 + C::RB + e % C::RB] = 0.f;
   }
   cluster.sync();
   for (int e = tid; e < kRows * C::RK; e += kThreads) {
