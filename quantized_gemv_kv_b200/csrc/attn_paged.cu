@@ -579,7 +579,8 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) attn_paged_kernel(const __gr
           sum += __shfl_xor_sync(0xffffffffu, sum, 1);
           sum += __shfl_xor_sync(0xffffffffu, sum, 2);
           // scores in base 2 from (16) sum X c
-          const float sc = finite ? __int_as_float((127 - (C::SPLIT ? 4 : 0) - kExp + e) << 23) * (A.scale * kLog2e) : NAN;
+          const float down = __int_as_float((127 - (C::SPLIT ? 4 : 0) - kExp + e) << 23);
+          const float sc = finite ? down * (A.scale * kLog2e) : NAN;
 #pragma unroll
           for (int z = 0; z < 2; ++z) {
             const int from = (col0 + z) * 4;
@@ -619,236 +620,238 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) attn_paged_kernel(const __gr
       // TILES tiles at a time; kept a loop, since a stage's whole code is more than the instruction cache likes.
 #pragma unroll 1
       for (int sub = 0; sub < TOK / C::SUB; ++sub) {
-      const unsigned char* st = stage + sub * TILES * C::TILEB;
-      const uint32_t* kpar = reinterpret_cast<const uint32_t*>(stage + C::PAR) + sub * C::SUB;
-      const uint32_t* vpar = kpar + TOK;
-      const int tok0 = (cons.q.st0 + cons.tile) * TOK + sub * C::SUB;
-      // a token of the step does not exist, or not every column sees every token
-      bool odd = false;
+        const unsigned char* st = stage + sub * TILES * C::TILEB;
+        const uint32_t* kpar = reinterpret_cast<const uint32_t*>(stage + C::PAR) + sub * C::SUB;
+        const uint32_t* vpar = kpar + TOK;
+        const int tok0 = (cons.q.st0 + cons.tile) * TOK + sub * C::SUB;
+        // a token of the step does not exist, or not every column sees every token
+        bool odd = false;
 #pragma unroll
-      for (int z = 0; z < C::SUB; z += 32) odd |= (kpar[z + lane] & 0xFFFFu) == 0;
-      odd = __any_sync(0xffffffffu, odd) || tok0 > all_hi - C::SUB || tok0 < all_lo;
+        for (int z = 0; z < C::SUB; z += 32) odd |= (kpar[z + lane] & 0xFFFFu) == 0;
+        odd = __any_sync(0xffffffffu, odd) || tok0 > all_hi - C::SUB || tok0 < all_lo;
 
-      // scores in base 2: tokens tok_of[k] x columns col0, col0 + 1
-      float s[TILES][NT][ROWS][2];
+        // scores in base 2: tokens tok_of[k] x columns col0, col0 + 1
+        float s[TILES][NT][ROWS][2];
 #pragma unroll
-      for (int j = 0; j < TILES; ++j) {
-        uint32_t wa[KW], wb[KW];
-        const unsigned char *kt = st + j * C::TILEB + k_off, *kb = kt + 8 * C::ROWB;
-        if constexpr (D == 64) {
-          *reinterpret_cast<uint2*>(wa) = *reinterpret_cast<const uint2*>(kt);
-          *reinterpret_cast<uint2*>(wb) = *reinterpret_cast<const uint2*>(kb);
-        } else {
-          *reinterpret_cast<uint4*>(wa) = *reinterpret_cast<const uint4*>(kt);
-          *reinterpret_cast<uint4*>(wb) = *reinterpret_cast<const uint4*>(kb);
-          if constexpr (D == 256) {
-            *reinterpret_cast<uint4*>(wa + 4) = *reinterpret_cast<const uint4*>(kt + (k_off1 - k_off));
-            *reinterpret_cast<uint4*>(wb + 4) = *reinterpret_cast<const uint4*>(kb + (k_off1 - k_off));
-          }
-        }
-        int d[NT][C::DT][C::SPLIT ? 2 : 1][4] = {};  // sums over the even codes, the odd ones (16 times)
-#pragma unroll
-        for (int w = 0; w < KW; w += 2)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            uint32_t a0, a1, a2, a3;
-            if constexpr (C::SPLIT) {  // words w and w + 1, even or odd codes
-              const uint32_t mask = e ? 0xF0F0F0F0u : 0x0F0F0F0Fu;
-              a0 = wa[w] & mask, a1 = wb[w] & mask, a2 = wa[w + 1] & mask, a3 = wb[w + 1] & mask;
-            } else {  // word w + e
-              a0 = wa[w + e] & 0x0F0F0F0Fu, a1 = wb[w + e] & 0x0F0F0F0Fu;
-              a2 = (wa[w + e] >> 4) & 0x0F0F0F0Fu, a3 = (wb[w + e] >> 4) & 0x0F0F0F0Fu;
+        for (int j = 0; j < TILES; ++j) {
+          uint32_t wa[KW], wb[KW];
+          const unsigned char *kt = st + j * C::TILEB + k_off, *kb = kt + 8 * C::ROWB;
+          if constexpr (D == 64) {
+            *reinterpret_cast<uint2*>(wa) = *reinterpret_cast<const uint2*>(kt);
+            *reinterpret_cast<uint2*>(wb) = *reinterpret_cast<const uint2*>(kb);
+          } else {
+            *reinterpret_cast<uint4*>(wa) = *reinterpret_cast<const uint4*>(kt);
+            *reinterpret_cast<uint4*>(wb) = *reinterpret_cast<const uint4*>(kb);
+            if constexpr (D == 256) {
+              *reinterpret_cast<uint4*>(wa + 4) = *reinterpret_cast<const uint4*>(kt + (k_off1 - k_off));
+              *reinterpret_cast<uint4*>(wb + 4) = *reinterpret_cast<const uint4*>(kb + (k_off1 - k_off));
             }
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int y = 0; y < C::DT; ++y)
-                imma(d[n][y][C::SPLIT ? e : 0], a0, a1, a2, a3, qb[n][w / 2][y][e][0], qb[n][w / 2][y][e][1]);
           }
-        // SPLIT: 16 sum d c, below 2^25 (256 dims: 2^26), so the three digits' sums are put together in fp32
-        auto digit = [&](int n, int y, int z) {
-          return C::SPLIT ? 16 * d[n][y][0][z] + d[n][y][C::SPLIT ? 1 : 0][z] : d[n][y][0][z];
-        };
+          int d[NT][C::DT][C::SPLIT ? 2 : 1][4] = {};  // sums over the even codes, the odd ones (16 times)
 #pragma unroll
-        for (int k = 0; k < ROWS; ++k) {
-          const uint32_t par = kpar[16 * j + tok_of[k]];
-          const float ks = sfd::half_bits_to_float(par & 0xFFFF), kz = sfd::half_bits_to_float(par >> 16);
+          for (int w = 0; w < KW; w += 2)
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              float f;  // sum X c, 16 times it if SPLIT
-              if constexpr (PACK) {
-                // lanes t and t ^ 2 hold digits 0 and 1 of both tokens: each takes the other's of its own token
-                const int mine_a = digit(n, 0, z), mine_b = digit(n, 0, 2 + z);
-                const int other = __shfl_xor_sync(0xffffffffu, t < 2 ? mine_b : mine_a, 2);
-                f = fmaf(static_cast<float>(t < 2 ? mine_a : mine_b), own_w, static_cast<float>(other) * other_w);
-                f = fmaf(static_cast<float>(t < 2 ? digit(n, 1, z) : digit(n, 1, 2 + z)), 65536.f, f);
-              } else {
-                f = C::SPLIT ? fmaf(static_cast<float>(digit(n, 1, 2 * k + z)), 256.f,
-                                    static_cast<float>(digit(n, 0, 2 * k + z)))
-                             : static_cast<float>(digit(n, 0, 2 * k + z) + 256 * digit(n, 1, 2 * k + z));
-                f = fmaf(static_cast<float>(digit(n, C::DT - 1, 2 * k + z)), 65536.f, f);
+            for (int e = 0; e < 2; ++e) {
+              uint32_t a0, a1, a2, a3;
+              if constexpr (C::SPLIT) {  // words w and w + 1, even or odd codes
+                const uint32_t mask = e ? 0xF0F0F0F0u : 0x0F0F0F0Fu;
+                a0 = wa[w] & mask, a1 = wb[w] & mask, a2 = wa[w + 1] & mask, a3 = wb[w + 1] & mask;
+              } else {  // word w + e
+                a0 = wa[w + e] & 0x0F0F0F0Fu, a1 = wb[w + e] & 0x0F0F0F0Fu;
+                a2 = (wa[w + e] >> 4) & 0x0F0F0F0Fu, a3 = (wb[w + e] >> 4) & 0x0F0F0F0Fu;
               }
-              s[j][n][k][z] = fmaf(-kz, qsum[n][z], f) * (ks * qsc[n][z]);
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int y = 0; y < C::DT; ++y)
+                  imma(d[n][y][C::SPLIT ? e : 0], a0, a1, a2, a3, qb[n][w / 2][y][e][0], qb[n][w / 2][y][e][1]);
             }
-          if (odd) {
-            const int tok = tok0 + 16 * j + tok_of[k];
-            const bool there = (par & 0xFFFFu) != 0;
+          // SPLIT: 16 sum d c, below 2^25 (256 dims: 2^26), so the three digits' sums are put together in fp32
+          auto digit = [&](int n, int y, int z) {
+            return C::SPLIT ? 16 * d[n][y][0][z] + d[n][y][C::SPLIT ? 1 : 0][z] : d[n][y][0][z];
+          };
+#pragma unroll
+          for (int k = 0; k < ROWS; ++k) {
+            const uint32_t par = kpar[16 * j + tok_of[k]];
+            const float ks = sfd::half_bits_to_float(par & 0xFFFF), kz = sfd::half_bits_to_float(par >> 16);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-              for (int z = 0; z < 2; ++z)
-                if (!there || tok >= lim_hi[n][z] || tok < lim_lo[n][z]) s[j][n][k][z] = -INFINITY;
+              for (int z = 0; z < 2; ++z) {
+                float f;  // sum X c, 16 times it if SPLIT
+                if constexpr (PACK) {
+                  // lanes t and t ^ 2 hold digits 0 and 1 of both tokens: each takes the other's of its own token
+                  const int mine_a = digit(n, 0, z), mine_b = digit(n, 0, 2 + z);
+                  const int other = __shfl_xor_sync(0xffffffffu, t < 2 ? mine_b : mine_a, 2);
+                  f = fmaf(static_cast<float>(t < 2 ? mine_a : mine_b), own_w, static_cast<float>(other) * other_w);
+                  f = fmaf(static_cast<float>(t < 2 ? digit(n, 1, z) : digit(n, 1, 2 + z)), 65536.f, f);
+                } else {
+                  f = C::SPLIT ? fmaf(static_cast<float>(digit(n, 1, 2 * k + z)), 256.f,
+                                      static_cast<float>(digit(n, 0, 2 * k + z)))
+                               : static_cast<float>(digit(n, 0, 2 * k + z) + 256 * digit(n, 1, 2 * k + z));
+                  f = fmaf(static_cast<float>(digit(n, C::DT - 1, 2 * k + z)), 65536.f, f);
+                }
+                s[j][n][k][z] = fmaf(-kz, qsum[n][z], f) * (ks * qsc[n][z]);
+              }
+            if (odd) {
+              const int tok = tok0 + 16 * j + tok_of[k];
+              const bool there = (par & 0xFFFFu) != 0;
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int z = 0; z < 2; ++z)
+                  if (!there || tok >= lim_hi[n][z] || tok < lim_lo[n][z]) s[j][n][k][z] = -INFINITY;
+            }
           }
         }
-      }
 
-      // the step's value scales and zero points
-      float vs[TILES][ROWS], vz[TILES][ROWS], vmax = 0.f;
+        // the step's value scales and zero points
+        float vs[TILES][ROWS], vz[TILES][ROWS], vmax = 0.f;
 #pragma unroll
-      for (int j = 0; j < TILES; ++j)
+        for (int j = 0; j < TILES; ++j)
 #pragma unroll
-        for (int k = 0; k < ROWS; ++k) {
-          uint32_t p = vpar[16 * j + tok_of[k]];
-          if (odd) {  // a token that no column sees may hold anything
-            const int tok = tok0 + 16 * j + tok_of[k];
-            if (tok < any_lo || tok >= any_hi || (kpar[16 * j + tok_of[k]] & 0xFFFFu) == 0) p = 0;
+          for (int k = 0; k < ROWS; ++k) {
+            uint32_t p = vpar[16 * j + tok_of[k]];
+            if (odd) {  // a token that no column sees may hold anything
+              const int tok = tok0 + 16 * j + tok_of[k];
+              if (tok < any_lo || tok >= any_hi || (kpar[16 * j + tok_of[k]] & 0xFFFFu) == 0) p = 0;
+            }
+            vs[j][k] = sfd::half_bits_to_float(p & 0xFFFF);
+            vz[j][k] = sfd::half_bits_to_float(p >> 16) - 8.f;
+            vmax = fmaxf(vmax, fabsf(vs[j][k]));
           }
-          vs[j][k] = sfd::half_bits_to_float(p & 0xFFFF);
-          vz[j][k] = sfd::half_bits_to_float(p >> 16) - 8.f;
-          vmax = fmaxf(vmax, fabsf(vs[j][k]));
-        }
 
-      // Raise the columns' references, and follow the largest value scale, when they have to: w = p v_s vscale stays
-      // below 2^4 2^11.
-      float top[NT][2];
-      bool raise = vmax * vscale >= 2048.f || (vscale == 0.f && vmax > 0.f);
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int z = 0; z < 2; ++z) {
-          top[n][z] = -INFINITY;
-#pragma unroll
-          for (int j = 0; j < TILES; ++j)
-#pragma unroll
-            for (int k = 0; k < ROWS; ++k) top[n][z] = fmaxf(top[n][z], s[j][n][k][z]);
-          raise |= top[n][z] > m[n][z] + 4.f;
-        }
-      if (__any_sync(0xffffffffu, raise)) {
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
-        float grow = 1.f;
-        if (vmax * vscale >= 2048.f || (vscale == 0.f && vmax > 0.f)) {
-          // 2^(10 - exponent of vmax), exact
-          const float next = __int_as_float((127 + 10 + 127 - (__float_as_int(vmax) >> 23)) << 23);
-          if (vscale != 0.f) grow = next / vscale;
-          vscale = next;
-        }
-        float alpha[NT][2];
+        // Raise the columns' references, and follow the largest value scale, when they have to: w = p v_s vscale stays
+        // below 2^4 2^11.
+        float top[NT][2];
+        bool raise = vmax * vscale >= 2048.f || (vscale == 0.f && vmax > 0.f);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int z = 0; z < 2; ++z) {
-            float mx = top[n][z];
+            top[n][z] = -INFINITY;
 #pragma unroll
-            for (int o = PACK ? 2 : 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            mx = fmaxf(m[n][z], mx + 2.f);
-            alpha[n][z] = mx == m[n][z] ? 1.f : ex2(m[n][z] - mx);  // 0 from -inf
-            m[n][z] = mx;
-            l[n][z] *= alpha[n][z];
-            alpha[n][z] *= grow;
-            zs[n][z] *= alpha[n][z];
+            for (int j = 0; j < TILES; ++j)
+#pragma unroll
+              for (int k = 0; k < ROWS; ++k) top[n][z] = fmaxf(top[n][z], s[j][n][k][z]);
+            raise |= top[n][z] > m[n][z] + 4.f;
           }
-        if (!empty) {
-        // the value product's columns 2t, 2t + 1 belong to the lane's score columns (packed: as weights or remainders)
+        if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-        for (int k = 0; k < MT; ++k)
+          for (int o = 1; o < 32; o <<= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
+          float grow = 1.f;
+          if (vmax * vscale >= 2048.f || (vscale == 0.f && vmax > 0.f)) {
+            // 2^(10 - exponent of vmax), exact
+            const float next = __int_as_float((127 + 10 + 127 - (__float_as_int(vmax) >> 23)) << 23);
+            if (vscale != 0.f) grow = next / vscale;
+            vscale = next;
+          }
+          float alpha[NT][2];
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int z = 0; z < 4; ++z) {
-              acc[k][n][z] *= alpha[n][z & 1];
-            }
-        if (has_flushed) {
-#pragma unroll 1
-          for (int k = 0; k < MT; ++k)
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              float4& f = flushed[(k * NT + n) * 32];
-              const float4 x = f;
-              f = make_float4(x.x * alpha[n][0], x.y * alpha[n][1], x.z * alpha[n][0], x.w * alpha[n][1]);
-            }
-        }
-        }
-      }
-      empty = false;
-
-      // weights as operand fragments
-      constexpr int WT = PACK ? 1 : 2;  // products of 8 columns per column tile
-      uint32_t bw[TILES][NT][WT][2];
-#pragma unroll
-      for (int j = 0; j < TILES; ++j)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          uint32_t hi2[ROWS], lo2[ROWS];
-#pragma unroll
-          for (int k = 0; k < ROWS; ++k) {
-            float w[2];
-#pragma unroll
             for (int z = 0; z < 2; ++z) {
-              const float p = ex2(s[j][n][k][z] - (m[n][z] == -INFINITY ? 0.f : m[n][z]));
-              l[n][z] += p;
-              w[z] = p * (vs[j][k] * vscale);
-              zs[n][z] = fmaf(w[z], vz[j][k], zs[n][z]);
-            }
-            const __half2 hh = __floats2half2_rn(w[0], w[1]);
-            hi2[k] = reinterpret_cast<const uint32_t&>(hh);
-            const float2 back = __half22float2(hh);
-            lo2[k] = h2_bits(w[0] - back.x, w[1] - back.y);
-          }
-          if constexpr (PACK) {
-            // columns 0-3 the weights, 4-7 the remainders: lanes t and t ^ 2 hold the two tokens of both
-            const uint32_t y = __shfl_xor_sync(0xffffffffu, t < 2 ? lo2[0] : hi2[0], 2);
-            bw[j][n][0][0] = transpose8x8(t < 2 ? hi2[0] : y);
-            bw[j][n][0][1] = transpose8x8(t < 2 ? y : lo2[0]);
-          } else {
+              float mx = top[n][z];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              bw[j][n][0][k] = transpose8x8(hi2[k]);
-              bw[j][n][WT - 1][k] = transpose8x8(lo2[k]);
+              for (int o = PACK ? 2 : 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+              mx = fmaxf(m[n][z], mx + 2.f);
+              alpha[n][z] = mx == m[n][z] ? 1.f : ex2(m[n][z] - mx);  // 0 from -inf
+              m[n][z] = mx;
+              l[n][z] *= alpha[n][z];
+              alpha[n][z] *= grow;
+              zs[n][z] *= alpha[n][z];
+            }
+          if (!empty) {
+            // the value product's columns 2t, 2t + 1 belong to the lane's score columns (packed: as weights or
+            // remainders)
+#pragma unroll
+            for (int k = 0; k < MT; ++k)
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                  acc[k][n][z] *= alpha[n][z & 1];
+                }
+            if (has_flushed) {
+#pragma unroll 1
+              for (int k = 0; k < MT; ++k)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                  float4& f = flushed[(k * NT + n) * 32];
+                  const float4 x = f;
+                  f = make_float4(x.x * alpha[n][0], x.y * alpha[n][1], x.z * alpha[n][0], x.w * alpha[n][1]);
+                }
             }
           }
         }
+        empty = false;
 
-      // values
+        // weights as operand fragments
+        constexpr int WT = PACK ? 1 : 2;  // products of 8 columns per column tile
+        uint32_t bw[TILES][NT][WT][2];
 #pragma unroll
-      for (int j = 0; j < TILES; ++j) {
-        uint32_t v[4][VW];  // tokens t, t + 4, t + 8, t + 12
+        for (int j = 0; j < TILES; ++j)
 #pragma unroll
-        for (int z = 0; z < 4; ++z) {
-          const unsigned char* vt = st + j * C::TILEB + ((z & 1) ? v_off1 : v_off0) + (z >> 1) * 8 * C::ROWB;
-          if constexpr (D == 64)
-            v[z][0] = *reinterpret_cast<const uint32_t*>(vt);
-          else if constexpr (D == 128)
-            *reinterpret_cast<uint2*>(v[z]) = *reinterpret_cast<const uint2*>(vt);
-          else
-            *reinterpret_cast<uint4*>(v[z]) = *reinterpret_cast<const uint4*>(vt);
-        }
+          for (int n = 0; n < NT; ++n) {
+            uint32_t hi2[ROWS], lo2[ROWS];
 #pragma unroll
-        for (int w = 0; w < VW; ++w)
+            for (int k = 0; k < ROWS; ++k) {
+              float w[2];
 #pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const uint32_t x0 = __byte_perm(v[0][w], v[1][w], b | (4 + b) << 8);
-            const uint32_t x1 = __byte_perm(v[2][w], v[3][w], b | (4 + b) << 8);
-            const uint32_t a0 = nib_lo(x0), a1 = nib_hi(x0), a2 = nib_lo(x1), a3 = nib_hi(x1);
+              for (int z = 0; z < 2; ++z) {
+                const float p = ex2(s[j][n][k][z] - (m[n][z] == -INFINITY ? 0.f : m[n][z]));
+                l[n][z] += p;
+                w[z] = p * (vs[j][k] * vscale);
+                zs[n][z] = fmaf(w[z], vz[j][k], zs[n][z]);
+              }
+              const __half2 hh = __floats2half2_rn(w[0], w[1]);
+              hi2[k] = reinterpret_cast<const uint32_t&>(hh);
+              const float2 back = __half22float2(hh);
+              lo2[k] = h2_bits(w[0] - back.x, w[1] - back.y);
+            }
+            if constexpr (PACK) {
+              // columns 0-3 the weights, 4-7 the remainders: lanes t and t ^ 2 hold the two tokens of both
+              const uint32_t y = __shfl_xor_sync(0xffffffffu, t < 2 ? lo2[0] : hi2[0], 2);
+              bw[j][n][0][0] = transpose8x8(t < 2 ? hi2[0] : y);
+              bw[j][n][0][1] = transpose8x8(t < 2 ? y : lo2[0]);
+            } else {
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              hmma(acc[4 * w + b][n], a0, a1, a2, a3, bw[j][n][0][0], bw[j][n][0][1]);
-              if constexpr (WT == 2) hmma(acc[4 * w + b][n], a0, a1, a2, a3, bw[j][n][WT - 1][0], bw[j][n][WT - 1][1]);
+              for (int k = 0; k < 2; ++k) {
+                bw[j][n][0][k] = transpose8x8(hi2[k]);
+                bw[j][n][WT - 1][k] = transpose8x8(lo2[k]);
+              }
             }
           }
-      }
+
+        // values
+#pragma unroll
+        for (int j = 0; j < TILES; ++j) {
+          uint32_t v[4][VW];  // tokens t, t + 4, t + 8, t + 12
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            const unsigned char* vt = st + j * C::TILEB + ((z & 1) ? v_off1 : v_off0) + (z >> 1) * 8 * C::ROWB;
+            if constexpr (D == 64)
+              v[z][0] = *reinterpret_cast<const uint32_t*>(vt);
+            else if constexpr (D == 128)
+              *reinterpret_cast<uint2*>(v[z]) = *reinterpret_cast<const uint2*>(vt);
+            else
+              *reinterpret_cast<uint4*>(v[z]) = *reinterpret_cast<const uint4*>(vt);
+          }
+#pragma unroll
+          for (int w = 0; w < VW; ++w)
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              const uint32_t x0 = __byte_perm(v[0][w], v[1][w], b | (4 + b) << 8);
+              const uint32_t x1 = __byte_perm(v[2][w], v[3][w], b | (4 + b) << 8);
+              const uint32_t a0 = nib_lo(x0), a1 = nib_hi(x0), a2 = nib_lo(x1), a3 = nib_hi(x1);
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                hmma(acc[4 * w + b][n], a0, a1, a2, a3, bw[j][n][0][0], bw[j][n][0][1]);
+                if constexpr (WT == 2)
+                  hmma(acc[4 * w + b][n], a0, a1, a2, a3, bw[j][n][WT - 1][0], bw[j][n][WT - 1][1]);
+              }
+            }
+        }
       }
 
       const bool ends = cons.tile + 1 == cons.q.stages || u + 1 == count;  // the segment's end, or the run's
@@ -928,7 +931,9 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) attn_paged_kernel(const __gr
                 if (g == 0) keep[C::COLS * D + col] = l[n][z] == 0.f ? -INFINITY : m[n][z] + log2f(l[n][z]);
               }
           }
-          if (lane == 0) parts[warp][which] = Part{lo + seg_at, lo + seg_end, keep, cons.q.row0, cons.q.rows, cons.block, cons.h};
+          if (lane == 0)
+            parts[warp][which] =
+                Part{lo + seg_at, lo + seg_end, keep, cons.q.row0, cons.q.rows, cons.block, cons.h};
         }
         fresh = true;
         seg_at = u + 1;
