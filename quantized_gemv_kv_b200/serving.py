@@ -73,6 +73,14 @@ def _same_device(first: str, **tensors) -> torch.device:
     return dev
 
 
+def _fit(**values: int) -> None:
+    """Whole numbers that go to the library as C ints, which ctypes would cut
+    to 32 bits without a word."""
+    for name, v in values.items():
+        if not -2 ** 31 <= v < 2 ** 31:
+            raise ValueError(f"{name} must fit 32 bits, it is {v}")
+
+
 def _ints(name: str, t: torch.Tensor, n: int | None = None) -> None:
     """A contiguous int32 vector, of n entries where n is given."""
     if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
@@ -178,6 +186,7 @@ class PagedKV:
             if s % last or (rows is not None and s // last != rows):
                 raise ValueError("the four arrays must have the same number of token-heads from page to page")
             rows = s // last
+        _fit(num_pages=self.num_pages, Hkv=self.Hkv, page_size=self.page_size, d=self.d)
         self._c = _PagedKV(self.k_codes.data_ptr(), self.k_param.data_ptr(), self.v_codes.data_ptr(),
                            self.v_param.data_ptr(), self.num_pages, self.Hkv, self.page_size, self.d, rows or 0)
 
@@ -221,6 +230,7 @@ class PagedPlan(_Job):
         _ints("n_free", n_free, 1)
         _ints("n_free_out", n_free_out, 1)
         stride = _table(block_table, R)
+        _fit(R=R, page_size=page_size, max_pages=block_table.shape[1], max_rows=max_rows, free_cap=free_list.numel())
         if max_rows < 1:
             raise ValueError("max_rows must be >= 1")
         dev = _same_device("lens", lens=lens, add=add, keep=keep, lens_out=lens_out, block_table=block_table,
@@ -287,6 +297,7 @@ class PagedAppend(_Job):
             qos = _matrix("q_out", q_out, torch.bfloat16, (T, Hq, d))
         elif q_out is not None:
             raise ValueError("q_out needs q")
+        _fit(T=T, Hq=Hq)
         for name, t in (("k_val", k_val), ("v_val", v_val)):
             if t is not None and (t.dtype != torch.bfloat16 or t.shape != (T, kv.Hkv, d) or not t.is_contiguous()):
                 raise ValueError(f"{name} must be contiguous bfloat16 {(T, kv.Hkv, d)}")
@@ -317,6 +328,7 @@ def paged_append(kv, k, v, slots, positions=None, theta=0.0, q=None, q_out=None,
 def attn_paged_workspace_size(T: int, R: int, Hq: int, Hkv: int, d: int, device=None) -> int:
     """Bytes of workspace that ``attn_paged`` needs on ``device`` (default:
     the current one); it goes by the device's number of SMs."""
+    _fit(T=T, R=R, Hq=Hq, Hkv=Hkv, d=d)
     out = _sz()
     with contextlib.nullcontext() if device is None else torch.cuda.device(device):
         _check(_lib.sf_attn_paged_workspace_size(T, R, Hq, Hkv, d, ctypes.byref(out)))
@@ -347,6 +359,7 @@ class PagedAttention(_Job):
         R = lens.numel()
         _ints("cu_rows", cu_rows, R + 1)
         stride = _table(block_table, R)
+        _fit(T=T, R=R, Hq=Hq, max_pages=block_table.shape[1], window=window)
         if out is None:
             out = torch.zeros((T, Hq, d), dtype=torch.float32, device=q.device)
         os_ = _matrix("out", out, tuple(_DTYPES), (T, Hq, d))
@@ -395,6 +408,7 @@ class LoraAdd(_Job):
         T, K = x.shape
         n, rank, _ = A.shape
         N = B.shape[1]
+        _fit(T=T, n_ids=ids.numel(), n_adapters=n, K=K, N=N, rank=rank)
         xs = _matrix("x", x, torch.bfloat16, (T, K))
         for name, t, shape in (("A", A, (n, rank, K)), ("B", B, (n, N, rank))):
             if t.dtype != torch.bfloat16 or tuple(t.shape) != shape or not t.is_contiguous():

@@ -1,6 +1,6 @@
 """Host-side rules of the serving binding that need no GPU: calls without rows,
 import on a PyTorch without the CUDA bindings, workspaces sized for the tensors'
-own device."""
+own device, integers that the C interface cannot hold."""
 
 import contextlib
 import ctypes
@@ -78,3 +78,24 @@ def test_workspace_is_sized_on_the_tensors_device(sf, monkeypatch):
     assert serving.attn_paged_workspace_size(3, 2, 4, 2, 128, device="cuda:1") == 4096
     assert serving.attn_paged_workspace_size(3, 2, 4, 2, 128) == 4096
     assert asked == [torch.device("cuda", 1), torch.device("cuda", 0)]
+
+
+@pytest.mark.parametrize("big", [2 ** 32 + 16, 2 ** 31, -(2 ** 32) + 16])
+def test_integers_beyond_32_bits_are_refused(sf, big):
+    """ctypes would cut them: a window of 2^32 + 16 would come out as one of 16 tokens."""
+    from quantized_gemv_kv_b200 import serving
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    plan = dict(lens=i32(3), add=i32(3), block_table=i32(3, 4), free_list=i32(9), n_free=i32(1), page_size=16,
+                max_rows=4)
+    for name in ("page_size", "max_rows"):
+        with pytest.raises(ValueError, match=name):
+            sf.PagedPlan(**{**plan, name: big})
+    with pytest.raises(ValueError, match="T must fit"):
+        sf.attn_paged_workspace_size(big, 2, 4, 2, 128)
+    param = torch.zeros((4, 2, 16, 2), dtype=torch.float16)
+    with pytest.MonkeyPatch.context() as mp:
+        mp.setattr(serving, "_dev", lambda t, name: None)
+        kv = serving.PagedKV(i32(4, 2, 16, 16), param, i32(4, 2, 16, 16), param)
+        with pytest.raises(ValueError, match="window must fit"):
+            serving.PagedAttention(torch.zeros((3, 4, 128), dtype=torch.bfloat16), kv, i32(3), i32(2), i32(2, 4),
+                                   window=big)
