@@ -886,8 +886,8 @@ sf_status sf_paged_append(const sf_paged_append_args* a, sf_stream_t stream);
  *           ends.
  * Scores are exact integer products of the codes with q in 22-bit fixed point
  * relative to its row's largest entry; softmax weights enter the value product
- * as f16 pairs (22 bits); all sums are fp32; a bf16 output is the fp32 one
- * rounded once.  A row whose q holds a NaN or Inf gives NaN.  The order of sums
+ * as f16 pairs (22 bits, and steps of 2^-33 of the largest value scale); all
+ * sums are fp32; a bf16 output is the fp32 one rounded once.  A row whose q holds a NaN or Inf gives NaN.  The order of sums
  * is fixed by the sizes and the values of len and cu_rows, so equal calls give
  * equal bits; a row beside other requests (or in a batch of other T or R) may
  * differ in its last bits, since its cache is then split elsewhere.

@@ -52,7 +52,7 @@ struct AttnArgs {
 //    tensor cores truncate their fp32 sums, so a chain of them drifts (7e-6 over
 //    a run of 112): after FLUSH stages the sums are added, rounded, to sums in
 //    shared memory and start again (128K tokens: 0.8e-6 off with a flush every 64
-//    tokens; every 256 in 3% less time, 1.4e-6; none in 5% less, 4.4e-6; sums in
+//    tokens; every 256 in 2% less time, 1.4e-6; none in 4% less, 4.4e-6; sums in
 //    the workspace instead cost 20%);
 //  * PACK, up to 4 columns (a decode step with 4 query heads per KV head): the
 //    score products' 16 columns are digit 0, digit 1 and twice digit 2 of the
@@ -60,7 +60,7 @@ struct AttnArgs {
 //    the value product's columns are the four weights and their four remainders:
 //    half the products.
 // The output's type decides nothing but the last rounding.  (Two digits of q and
-// weights without remainders for bf16 outputs take 16% less time, 188 us for 223
+// weights without remainders for bf16 outputs take 23% less time, 185 us for 241
 // with 64 requests of 1 to 4 rows, but lose bits of every channel below a
 // query's largest, and show in the bf16 output.)
 // The k index of the value product is free, so the tokens of a tile are
@@ -79,7 +79,7 @@ struct Cfg {
   static constexpr bool PACK = PACK_;
   static constexpr int FLUSH = 64 / TOK;  // stages
   static constexpr int COLS = PACK ? 4 : 8 * NT, GROUPS = TOK / 16;
-  // tiles and tokens of a step of the inner loop: four tiles where the registers allow (128K tokens: 42 us; two, 45)
+  // tiles and tokens of a step of the inner loop: four tiles where the registers allow (128K tokens: 44 us; two, 47)
   static constexpr int TILES = NT == 1 && D <= 128 && WARPS == 8 ? 4 : 2, SUB = 16 * TILES;
   static_assert(TOK % SUB == 0, "whole steps");
   static constexpr bool SPLIT = NT == 1;  // odd codes as 16 c in sums of their own: fewer shifts, more sums
@@ -1074,8 +1074,8 @@ struct Kernel {
 };
 
 // Calls f with the kernel for these sizes: 4 (packed), 8 or 16 columns a block, by the columns that a request's rows
-// fill on average (rounded down: a padded batch has a few rows more than its requests); d = 256 has no registers for
-// 16.
+// fill on average (rounded down: a padded batch has a few rows more than its requests; one padded to many more runs a
+// wider kernel than it needs: right, but slower); d = 256 has no registers for 16.
 template <class F>
 auto with_kernel(int T, int R, int Hq, int Hkv, int d, F f) {
   const int64_t cols = static_cast<int64_t>(std::max(1, T / R)) * (Hq / Hkv);

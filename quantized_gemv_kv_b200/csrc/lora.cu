@@ -414,8 +414,10 @@ extern "C" sf_status sf_lora_add(const sf_lora_args* a, sf_stream_t stream) {
   while (P.log_blocks > 0 && static_cast<int64_t>(windows) << P.log_blocks > 2 * room) --P.log_blocks;
   const int most = ((a->T > 512 ? 4 * room : room) >> P.log_blocks) / windows;
   P.share = std::max(1, std::min({P.window, a->T, a->n_adapters, most}));
-  // A projection's outputs are shared by two clusters while the SMs have room (64 rows, 16 adapters of rank 64, N =
-  // 14336: 22 us; one cluster each takes 14% longer, clusters of 16 blocks instead 60%).
+  // A wide projection's outputs are shared by two clusters while the SMs have room (64 rows, 16 adapters of rank 64, N =
+  // 14336: 22 us; one cluster each takes 14% longer, clusters of 16 blocks instead 60%.  4 rows of rank 64, N = 4096 /
+  // 2048 / 1024: 9.3 / 8.9 / 8.8 us shared, 10.6 / 9.3 / 8.9 not; but 16 rows of rank 16, N = 1024: 8.0 and 7.6, 64 rows
+  // of rank 64, N = 1024: 12.8 and 12.3).
   P.log_split = P.few && a->N >= 2048 && static_cast<int64_t>(windows) * P.share * 2 << P.log_blocks <= room;
   SF_REQUIRE(static_cast<int64_t>(windows) * P.share << P.log_blocks < (1ll << 30), "%s: T is too large", what);
   cudaStream_t s = sf::as_cuda(stream);
