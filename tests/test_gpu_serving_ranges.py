@@ -1,6 +1,7 @@
 """The serving operators at the ends of their ranges: page numbers that no pool
 has, plans made by several host threads, rotations bit by bit, token-heads of
-every size, long inner loops of the adapters, values near the largest float."""
+every size, long inner loops of the adapters, values near the largest float,
+captured steps."""
 
 import threading
 
@@ -228,3 +229,60 @@ def test_lora_near_the_largest_float(sf, rank):
     out = sf.lora_add(x.cuda(), A.cuda(), B.cuda(), scale.cuda(), _i32([0, 0]), y=torch.zeros((2, N), device="cuda"))
     want = x[:, 3:4].double() * scale.double() * 2.0 ** 127 * B[0, :, 5].double()
     assert torch.all((out.cpu().double() - want).abs() <= 2.0 ** -22 * want.abs())
+
+
+# ---- a step of all of them, captured -------------------------------------------------
+
+
+def test_captured_steps_equal_eager_ones(sf):
+    """Plan, adapters, append with RoPE and attention of a decode loop, replayed from one graph as often as called one by
+    one: the same lengths, pages, pool and outputs, bit for bit, in a batch padded to twice its rows."""
+    Hq, Hkv, d, H, P, R, MP, rows, pages = 8, 2, 128, 256, 16, 5, 12, 40, 64
+    N = (Hq + 2 * Hkv) * d
+    x, A, B, scale, _ = _lora(rows, H, N, 16, 3, 90)
+    base = torch.randn((rows, N), generator=torch.Generator(device="cuda").manual_seed(91), device="cuda")
+    ids = _i32([2, -1, 0, 1, 2])
+
+    class Loop:
+        def __init__(self):
+            self.lens, self.n_free = _i32([0] * R), _i32([pages])
+            self.table, self.free = _i32(np.full((R, MP), -1)), _i32(np.arange(pages))
+            self.keep, self.add = _i32([0] * R), _i32([0] * R)
+            self.plan = sf.PagedPlan(self.lens, self.add, self.table, self.free, self.n_free, P, rows, keep=self.keep)
+            self.kv = sf.PagedKV.empty(pages, Hkv, P, d)
+            self.qkv = torch.zeros((rows, N), device="cuda")
+            q, k, v = (self.qkv[:, a * d:b * d].unflatten(1, (b - a, d)) for a, b in
+                       ((0, Hq), (Hq, Hq + Hkv), (Hq + Hkv, N // d)))
+            self.lora = sf.LoraAdd(x, A, B, scale, ids, self.qkv, base, row_of=self.plan.row_request)
+            self.append = sf.PagedAppend(self.kv, k, v, self.plan.slots, self.plan.positions, 10000.0, q,
+                                         torch.zeros((rows, Hq, d), dtype=torch.bfloat16, device="cuda"))
+            self.attn = sf.PagedAttention(self.append.q_out, self.kv, self.plan.cu_rows, self.lens, self.table)
+
+        def step(self):
+            for job in (self.plan, self.lora, self.append, self.attn):
+                job.run()
+
+        def state(self):
+            kv = self.kv
+            return (self.lens, self.n_free, self.table, self.plan.slots, self.plan.status, self.qkv, self.append.q_out,
+                    kv.k_codes, kv.k_param, kv.v_codes, kv.v_param, self.attn.out)
+
+    eager, replayed = Loop(), Loop()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        replayed.step()
+    lens = [0] * R
+    rng = np.random.default_rng(92)
+    for _ in range(12):
+        keep = [int(n if rng.random() < 0.7 else rng.integers(0, n + 1)) for n in lens]
+        add = [int(min(rng.integers(0, 5), MP * P - k)) for k in keep]
+        for loop in (eager, replayed):
+            loop.keep.copy_(_i32(keep))
+            loop.add.copy_(_i32(add))
+        eager.step()
+        graph.replay()
+        torch.cuda.synchronize()
+        lens = [k + a for k, a in zip(keep, add)]
+        assert eager.lens.tolist() == lens
+        for a, b in zip(eager.state(), replayed.state()):
+            assert torch.equal(a, b)
